@@ -44,7 +44,9 @@ EXPORTS = ("qlinear_quantize_weight", "qlinear_quantize_act", "qlinear_gemv", "q
            "qlinear_gemv_prequant", "qlinear_gemm_small_prequant",
            "qlinear_gemm_quant_out", "qlinear_weight_only_workspace_bytes", "qlinear_gemm_grouped",
            "qlinear_gemm_grouped_workspace_bytes", "qlinear_gemm_small_grouped",
-           "qlinear_gemm_small_grouped_workspace_bytes")
+           "qlinear_gemm_small_grouped_workspace_bytes", "qlinear_quantize_weight_w4",
+           "qlinear_forward_w4", "qlinear_forward_w4_workspace_bytes", "qlinear_route",
+           "qlinear_experts_w4", "qlinear_experts_w4_workspace_bytes")
 
 
 class QLinearError(RuntimeError):
@@ -112,6 +114,14 @@ def lib() -> ctypes.CDLL:
         L.qlinear_workspace_bytes.restype = sz
         L.qlinear_forward_workspace_bytes.argtypes = [i32, i64, i64, i64]
         L.qlinear_forward_workspace_bytes.restype = sz
+        L.qlinear_quantize_weight_w4.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp]
+        L.qlinear_forward_w4.argtypes = [vp, vp, i64, vp, vp, sz, vp]
+        L.qlinear_forward_w4_workspace_bytes.argtypes = [i64, vp]
+        L.qlinear_forward_w4_workspace_bytes.restype = sz
+        L.qlinear_route.argtypes = [vp, i32, vp, vp, i64, vp, vp, vp]
+        L.qlinear_experts_w4.argtypes = [vp, vp, vp, vp, i64, i64, vp, vp, sz, vp]
+        L.qlinear_experts_w4_workspace_bytes.argtypes = [i64, i64, vp, i32]
+        L.qlinear_experts_w4_workspace_bytes.restype = sz
         L.qlinear_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         L.qlinear_status_string.argtypes = [i32]
         L.qlinear_status_string.restype = ctypes.c_char_p
@@ -122,7 +132,8 @@ def lib() -> ctypes.CDLL:
                      "qlinear_gemv_weight_only", "qlinear_debug_gemv_stalled",
                      "qlinear_forward_weight_only", "qlinear_gemv_grouped",
                      "qlinear_gemv_prequant", "qlinear_gemm_small_prequant",
-                     "qlinear_gemm_quant_out"):
+                     "qlinear_gemm_quant_out", "qlinear_quantize_weight_w4", "qlinear_forward_w4",
+                     "qlinear_route", "qlinear_experts_w4"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -510,6 +521,186 @@ def forward(scheme: int, x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
                                  _dev(sw, torch.float32, "sw"), M, N, K,
                                  _dev(y, torch.bfloat16, "y"), wp, wn, _stream(stream)),
            "qlinear_forward")
+    return y
+
+
+# ---------------------------------------------------------------- 4-bit weights, experts
+
+
+def _on(t: torch.Tensor, dtype, name: str, device: int) -> int:
+    """_dev, and on the device the call launches on."""
+    p = _dev(t, dtype, name)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call runs on cuda:{device}")
+    return p
+
+
+class _W4(ctypes.Structure):
+    _fields_ = [("wq", ctypes.c_void_p), ("sw", ctypes.c_void_p), ("wz", ctypes.c_void_p),
+                ("experts", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("group", ctypes.c_int64)]
+
+
+W4_GROUPS = (32, 64, 128)
+
+
+class W4Weight:
+    """4-bit weights with group scales: w[n,k] = (q[n,k] - z[n,k//group]) * s[n,k//group].
+
+    wq uint8 [N,K/2] (low nibble: even k) or, for experts, [E,N,K/2]; sw bfloat16
+    [(E,)N,ceil(K/group)]; wz uint8 of sw's shape, or None for a zero point of 8.
+    The tensors are checked once and kept; their contents may change."""
+
+    __slots__ = ("wq", "sw", "wz", "group", "experts", "N", "K", "device", "_c", "_p")
+
+    def __init__(self, wq: torch.Tensor, sw: torch.Tensor, wz: torch.Tensor | None = None, group: int = 128):
+        if group not in W4_GROUPS:
+            raise ValueError(f"group must be one of {W4_GROUPS}")
+        if wq.dim() not in (2, 3):
+            raise ValueError("wq must be [N,K/2] or [E,N,K/2]")
+        if not isinstance(wq, torch.Tensor) or not wq.is_cuda:
+            raise TypeError("wq must be a CUDA tensor")
+        K = 2 * wq.shape[-1]
+        shape = tuple(wq.shape[:-1]) + (-(-K // group),)
+        if tuple(sw.shape) != shape or (wz is not None and tuple(wz.shape) != shape):
+            raise ValueError(f"scales and zero points must be {shape} for these codes and group {group}")
+        self.device = wq.get_device()
+        self.wq, self.sw, self.wz, self.group = wq, sw, wz, group
+        self.experts = wq.shape[0] if wq.dim() == 3 else 1
+        self.N, self.K = wq.shape[-2], K
+        self._c = _W4(_on(wq, torch.uint8, "wq", self.device), _on(sw, torch.bfloat16, "sw", self.device),
+                      None if wz is None else _on(wz, torch.uint8, "wz", self.device), self.experts, self.N, K, group)
+        self._p = ctypes.addressof(self._c)
+
+
+def quantize_weight_w4(w: torch.Tensor, group: int = 128, zeros: bool = False, stream=None) -> W4Weight:
+    """bf16 weights [N,K] or [E,N,K] -> W4Weight (see qlinear_quantize_weight_w4)."""
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [N,K] or [E,N,K]")
+    K = w.shape[-1]
+    if group not in W4_GROUPS or K % 32:
+        raise ValueError(f"K must be a multiple of 32 and group one of {W4_GROUPS}")
+    lead = tuple(w.shape[:-1])
+    wp = _on(w, torch.bfloat16, "w", torch.cuda.current_device())
+    wq = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=w.device)
+    sw = torch.empty(lead + (-(-K // group),), dtype=torch.bfloat16, device=w.device)
+    wz = torch.empty_like(sw, dtype=torch.uint8) if zeros else None
+    _check(lib().qlinear_quantize_weight_w4(wp, w.numel() // K, K, group, wq.data_ptr(), sw.data_ptr(),
+                                            None if wz is None else wz.data_ptr(), _stream(stream)),
+           "qlinear_quantize_weight_w4")
+    return W4Weight(wq, sw, wz, group)
+
+
+def forward_w4_workspace_bytes(M: int, w: W4Weight) -> int:
+    return int(lib().qlinear_forward_w4_workspace_bytes(M, w._p))
+
+
+def forward_w4(x: torch.Tensor, w: W4Weight, workspace: torch.Tensor | None = None, y=None,
+               stream=None) -> torch.Tensor:
+    """y = x W^T with 4-bit weights: x bf16 [M,K] (not rounded) -> y bf16 [M,N], any M."""
+    M, K = x.shape
+    if K != w.K or w.wq.dim() != 2:
+        raise ValueError(f"x {tuple(x.shape)} does not fit weights [{w.N},{w.K}] of one layer")
+    dev = torch.cuda.current_device()
+    if w.device != dev:
+        raise ValueError(f"the weights are on cuda:{w.device}, the current device is cuda:{dev}")
+    L = lib()
+    if workspace is None:
+        nb = L.qlinear_forward_w4_workspace_bytes(M, w._p)
+        workspace = _scratch(nb, stream) if nb else None
+    if y is None:
+        y = torch.empty((M, w.N), dtype=torch.bfloat16, device=x.device)
+    elif tuple(y.shape) != (M, w.N):
+        raise ValueError(f"y must be {(M, w.N)}")
+    wp, wn = (None, 0) if workspace is None else (_on(workspace, torch.uint8, "workspace", dev), workspace.numel())
+    _check(L.qlinear_forward_w4(_on(x, torch.bfloat16, "x", dev), w._p, M, _on(y, torch.bfloat16, "y", dev), wp, wn,
+                                _stream(stream)), "qlinear_forward_w4")
+    return y
+
+
+def _scratch(nbytes: int, stream) -> torch.Tensor:
+    """Scratch for one call, allocated on the call's stream so that the caching
+    allocator hands it out again only behind the call's work."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+ROUTE_SOFTMAX = 0
+ROUTE_SIGMOID = 1
+
+
+class _RouteConfig(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int64), ("top_k", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("top_groups", ctypes.c_int64), ("group_top", ctypes.c_int64), ("score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+def route(logits: torch.Tensor, top_k: int, score: int = ROUTE_SOFTMAX, bias: torch.Tensor | None = None,
+          groups: int = 1, top_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+          ids=None, weights=None, stream=None):
+    """Router: logits f32 or bf16 [T,E] -> (ids int32 [T,top_k], weights f32 [T,top_k]).
+    Scores by softmax or sigmoid, `bias` f32 [E] for the choice only, limited groups,
+    ties to the lower index (see qlinear_route)."""
+    T, E = logits.shape
+    dev = torch.cuda.current_device()
+    bf16 = logits.dtype == torch.bfloat16
+    if not bf16 and logits.dtype != torch.float32:
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    lp = _on(logits, logits.dtype, "logits", dev)
+    bp = None
+    if bias is not None:
+        bp = _on(bias, torch.float32, "bias", dev)
+        if bias.numel() != E:
+            raise ValueError(f"bias must have {E} entries")
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    if tuple(ids.shape) != (T, top_k) or tuple(weights.shape) != (T, top_k):
+        raise ValueError(f"ids and weights must be {(T, top_k)}")
+    c = _RouteConfig(E, top_k, groups, top_groups, group_top, score, bool(renormalize), scale)
+    _check(lib().qlinear_route(lp, bf16, ctypes.addressof(c), bp, T, _on(ids, torch.int32, "ids", dev),
+                               _on(weights, torch.float32, "weights", dev), _stream(stream)), "qlinear_route")
+    return ids, weights
+
+
+def experts_w4_workspace_bytes(T: int, top_k: int, w: W4Weight, combine: bool = False) -> int:
+    return int(lib().qlinear_experts_w4_workspace_bytes(T, top_k, w._p, combine))
+
+
+def experts_w4(x: torch.Tensor, ids: torch.Tensor, w: W4Weight, weights: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, y=None, stream=None) -> torch.Tensor:
+    """The routed tokens' products with their experts' 4-bit weights, ids int32 [T,k]:
+    x bf16 [T,K] -> y bf16 [T,k,N], or with `weights` f32 [T,k] x bf16 [T,k,K] ->
+    y bf16 [T,N], each token's experts summed (see qlinear_experts_w4)."""
+    T, k = ids.shape
+    combine = weights is not None
+    if w.wq.dim() != 3 or tuple(x.shape) != ((T, k, w.K) if combine else (T, w.K)):
+        raise ValueError(f"x {tuple(x.shape)} does not fit ids {(T, k)} and experts [{w.experts},{w.N},{w.K}]")
+    dev = torch.cuda.current_device()
+    if w.device != dev:
+        raise ValueError(f"the weights are on cuda:{w.device}, the current device is cuda:{dev}")
+    L = lib()
+    gp = None
+    if combine:
+        gp = _on(weights, torch.float32, "weights", dev)
+        if tuple(weights.shape) != (T, k):
+            raise ValueError(f"weights must be {(T, k)}")
+    if workspace is None:
+        nb = L.qlinear_experts_w4_workspace_bytes(T, k, w._p, combine)
+        workspace = _scratch(nb, stream) if nb else None
+    shape = (T, w.N) if combine else (T, k, w.N)
+    if y is None:
+        y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    elif tuple(y.shape) != shape:
+        raise ValueError(f"y must be {shape}")
+    wp, wn = (None, 0) if workspace is None else (_on(workspace, torch.uint8, "workspace", dev), workspace.numel())
+    _check(L.qlinear_experts_w4(_on(x, torch.bfloat16, "x", dev), _on(ids, torch.int32, "ids", dev), gp, w._p, T, k,
+                                _on(y, torch.bfloat16, "y", dev), wp, wn, _stream(stream)), "qlinear_experts_w4")
     return y
 
 

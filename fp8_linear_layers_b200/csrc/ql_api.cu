@@ -610,3 +610,124 @@ extern "C" ql_status qlinear_gemm_small_noalloc(ql_scheme scheme, const uint16_t
                             d.sms, d.status, st);
   return e == cudaSuccess ? QL_OK : cuda_fail(e, "qlinear_gemm_small_noalloc");
 }
+
+// ---------------------------------------------------------------------------
+// 4-bit weights, routing, experts
+// ---------------------------------------------------------------------------
+namespace {
+
+// The shape of a 4-bit matrix; the pointers are checked by check_w4_pointers.
+ql_status check_w4_shape(const ql_w4_weight* w) {
+  if (!w || w->N <= 0 || w->K <= 0 || w->experts <= 0) return QL_ERR_INVALID_ARG;
+  if (w->group != 32 && w->group != 64 && w->group != 128) return QL_ERR_UNSUPPORTED_SHAPE;
+  if (w->K % 32 || w->K >= kIndexLimit || w->N >= kIndexLimit || w->experts >= kIndexLimit ||
+      w->experts * w->N >= kIndexLimit)
+    return QL_ERR_UNSUPPORTED_SHAPE;
+  return QL_OK;
+}
+
+ql_status check_w4_pointers(const ql_w4_weight* w) {
+  QL_TRY(need(w->wq));
+  QL_TRY(need(w->sw));
+  if (w->wz && !aligned16(w->wz)) return QL_ERR_MISALIGNED;
+  return QL_OK;
+}
+
+ql_status check_w4_experts(const ql_w4_weight* w, int64_t T, int64_t top_k) {
+  QL_TRY(check_w4_shape(w));
+  if (T < 0 || top_k < 1 || top_k > QL_ROUTE_MAX_TOP_K) return QL_ERR_INVALID_ARG;
+  if (w->experts > QL_ROUTE_MAX_EXPERTS || T >= kIndexLimit / QL_ROUTE_MAX_TOP_K) return QL_ERR_UNSUPPORTED_SHAPE;
+  return QL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ql_status qlinear_quantize_weight_w4(const uint16_t* w, int64_t N, int64_t K, int64_t group, void* wq,
+                                     uint16_t* sw, uint8_t* wz, void* stream) {
+  const ql_w4_weight shape{wq, sw, wz, 1, N, K, group};
+  QL_TRY(check_w4_shape(&shape));
+  if (N * (K / 8) >= kIndexLimit * 64) return QL_ERR_UNSUPPORTED_SHAPE;  // the grid
+  QL_TRY(need(w));
+  QL_TRY(check_w4_pointers(&shape));
+  DeviceInfo d;
+  QL_TRY(current_device(&d));
+  cudaError_t e = ql::launch_quantize_w4(w, N, K, group, static_cast<uint8_t*>(wq), sw, wz,
+                                         static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QL_OK : cuda_fail(e, "qlinear_quantize_weight_w4");
+}
+
+size_t qlinear_forward_w4_workspace_bytes(int64_t M, const ql_w4_weight* w) {
+  (void)M;
+  (void)w;
+  return 0;
+}
+
+ql_status qlinear_forward_w4(const uint16_t* x, const ql_w4_weight* w, int64_t M, uint16_t* y,
+                             void* workspace, size_t ws_bytes, void* stream) {
+  QL_TRY(check_w4_shape(w));
+  if (w->experts != 1 || M < 0) return QL_ERR_INVALID_ARG;
+  if (M >= kIndexLimit) return QL_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return QL_OK;
+  QL_TRY(need(x));
+  QL_TRY(check_w4_pointers(w));
+  QL_TRY(need(y));
+  (void)workspace;
+  (void)ws_bytes;
+  DeviceInfo d;
+  QL_TRY(current_device(&d));
+  cudaError_t e = ql::launch_w4_stream(x, *w, M, y, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QL_OK : cuda_fail(e, "qlinear_forward_w4");
+}
+
+ql_status qlinear_route(const void* logits, int logits_bf16, const ql_route_config* c, const float* bias,
+                        int64_t T, int32_t* ids, float* weights, void* stream) {
+  if (!c || T < 0 || c->experts <= 0 || c->groups <= 0) return QL_ERR_INVALID_ARG;
+  if (c->score != QL_ROUTE_SOFTMAX && c->score != QL_ROUTE_SIGMOID) return QL_ERR_INVALID_ARG;
+  if (c->top_k < 1 || c->top_k > c->experts || c->top_k > QL_ROUTE_MAX_TOP_K) return QL_ERR_INVALID_ARG;
+  if (c->group_top != 1 && c->group_top != 2) return QL_ERR_INVALID_ARG;
+  if (c->experts > QL_ROUTE_MAX_EXPERTS || c->groups > QL_ROUTE_MAX_GROUPS || c->experts % c->groups ||
+      c->top_groups < 1 || c->top_groups > c->groups || c->experts / c->groups < c->group_top ||
+      c->top_groups * (c->experts / c->groups) < c->top_k)
+    return QL_ERR_UNSUPPORTED_SHAPE;
+  if (T >= kIndexLimit) return QL_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return QL_OK;
+  QL_TRY(need(logits));
+  if (bias && !aligned16(bias)) return QL_ERR_MISALIGNED;
+  QL_TRY(need(ids));
+  QL_TRY(need(weights));
+  DeviceInfo d;
+  QL_TRY(current_device(&d));
+  cudaError_t e = ql::launch_route(logits, logits_bf16 != 0, *c, bias, T, ids, weights,
+                                   static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QL_OK : cuda_fail(e, "qlinear_route");
+}
+
+size_t qlinear_experts_w4_workspace_bytes(int64_t T, int64_t top_k, const ql_w4_weight* w, int combine) {
+  (void)T;
+  (void)top_k;
+  (void)w;
+  (void)combine;
+  return 0;
+}
+
+ql_status qlinear_experts_w4(const uint16_t* x, const int32_t* ids, const float* weights, const ql_w4_weight* w,
+                             int64_t T, int64_t top_k, uint16_t* y, void* workspace, size_t ws_bytes,
+                             void* stream) {
+  QL_TRY(check_w4_experts(w, T, top_k));
+  if (T == 0) return QL_OK;
+  QL_TRY(need(x));
+  QL_TRY(need(ids));
+  if (weights && !aligned16(weights)) return QL_ERR_MISALIGNED;
+  QL_TRY(check_w4_pointers(w));
+  QL_TRY(need(y));
+  (void)workspace;
+  (void)ws_bytes;
+  DeviceInfo d;
+  QL_TRY(current_device(&d));
+  cudaError_t e = ql::launch_w4_stream_experts(x, ids, weights, *w, T, top_k, y, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QL_OK : cuda_fail(e, "qlinear_experts_w4");
+}
+
+}  // extern "C"

@@ -120,4 +120,14 @@ cudaError_t launch_gemm_small(ql_scheme scheme, const uint16_t* x, const void* w
                               DevStatus* status, cudaStream_t st, const uint8_t* pre_qx = nullptr,
                               const float* pre_sx = nullptr);
 
+// 4-bit weights: few tokens on mma.sync, one pass over the weights for each 16
+// (dense) or 8 (experts) tokens.
+cudaError_t launch_w4_stream(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint16_t* y, cudaStream_t st);
+cudaError_t launch_w4_stream_experts(const uint16_t* x, const int32_t* ids, const float* weights,
+                                     const ql_w4_weight& w, int64_t T, int64_t topk, uint16_t* y, cudaStream_t st);
+cudaError_t launch_quantize_w4(const uint16_t* w, int64_t N, int64_t K, int64_t group, uint8_t* wq, uint16_t* sw,
+                               uint8_t* wz, cudaStream_t st);
+cudaError_t launch_route(const void* logits, bool bf16, const ql_route_config& c, const float* bias, int64_t T,
+                         int32_t* ids, float* weights, cudaStream_t st);
+
 }  // namespace ql

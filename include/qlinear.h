@@ -412,6 +412,120 @@ ql_status qlinear_forward(ql_scheme scheme, const uint16_t* x, const void* wq, c
 size_t qlinear_workspace_bytes(ql_scheme scheme, int64_t M, int64_t N, int64_t K);
 size_t qlinear_forward_workspace_bytes(ql_scheme scheme, int64_t M, int64_t N, int64_t K);
 
+/* ------------------------------------------------- 4-bit weights, experts */
+
+/* A matrix of 4-bit weights with a scale for each group of inputs, and, for a
+ * mixture of experts, one such matrix for each expert:
+ *   w[n,k] = (q[n,k] - z[n,k/group]) * s[n,k/group]
+ *   wq     device, codes q in 0..15, two to a byte along K: [experts,N,K/2]
+ *          bytes, byte j of a row holding input 2j (low nibble) and 2j+1 (high)
+ *   sw     device, scales s as bf16 patterns: [experts,N,ceil(K/group)]
+ *   wz     device, zero points z in 0..15, one byte each, laid out like sw; or
+ *          NULL: z = 8 everywhere
+ *   group  32, 64 or 128 inputs; the last group of a row may be shorter
+ * Host struct, read during the call only.  K % 32 == 0, N and K below 2^31,
+ * experts * N below 2^31; experts is 1 for a dense layer. */
+typedef struct ql_w4_weight {
+  const void* wq;
+  const uint16_t* sw;
+  const uint8_t* wz;
+  int64_t experts;
+  int64_t N;
+  int64_t K;
+  int64_t group;
+} ql_w4_weight;
+
+/* Quantizes bf16 weights to 4 bits in groups along K (offline, checkpoint side):
+ *   wz NULL:  s = bf16(absmax / 7),      q = clamp(rne(w / s), -7, 7) + 8
+ *   wz given: s = bf16((hi - lo) / 15),  z = clamp(rne(-lo / s), 0, 15),
+ *             q = clamp(rne(w / s) + z, 0, 15), lo = min(0, w), hi = max(0, w)
+ * over the group, IEEE f32 divisions of finite weights; a group of scale zero
+ * gets codes and zero points 8.
+ *   w   device, bf16 [N,K] (experts: stack their rows, N = experts * rows)
+ *   wq  device, out: [N,K/2];  sw  device, out: bf16 [N,ceil(K/group)]
+ *   wz  device, out: [N,ceil(K/group)], or NULL
+ * Errors: argument checks as above; group not 32, 64 or 128, K % 32 != 0 ->
+ * QL_ERR_UNSUPPORTED_SHAPE. */
+ql_status qlinear_quantize_weight_w4(const uint16_t* w, int64_t N, int64_t K, int64_t group, void* wq,
+                                     uint16_t* sw, uint8_t* wz, void* stream);
+
+/* Product with 4-bit weights, activations not rounded (weight-only numerics):
+ *   y[m,n] = bf16_rne( sum_k x[m,k] * w[n,k] ),
+ * products exact, sums in f32.  Any M: a few tokens stream the weights once, more
+ * run on the tcgen05 tensor cores.
+ *   x          device, bf16 [M,K];  y  device, out: bf16 [M,N]
+ *   w          experts = 1
+ *   workspace  device, qlinear_forward_w4_workspace_bytes(M, w) bytes (0: none
+ *              needed, NULL allowed), 256-byte aligned.  Scratch: its contents
+ *              before a call do not matter.  Calls in flight together must not
+ *              share it.
+ * Unlike the 8-bit products, wq, sw and wz may be written by earlier work on the
+ * same stream.
+ * Errors: argument checks as above; M = 0 is a no-op; QL_ERR_WORKSPACE. */
+ql_status qlinear_forward_w4(const uint16_t* x, const ql_w4_weight* w, int64_t M, uint16_t* y,
+                             void* workspace, size_t ws_bytes, void* stream);
+size_t qlinear_forward_w4_workspace_bytes(int64_t M, const ql_w4_weight* w);
+
+/* Routing of T tokens to experts.  With l the token's logits:
+ *   p    softmax(l) or sigmoid(l) for each expert
+ *   c    p + bias, or, without a bias, l itself (the order of p)
+ *   groups > 1: the experts fall into `groups` equal ranges; a range's value is
+ *        its largest c (group_top = 1) or the sum of its two largest (group_top
+ *        = 2; without a bias, of p), and only the top_groups best ranges stay
+ *   ids  the top_k largest c in descending order
+ *   w_j  p[ids_j], divided by their sum if `renormalize`, times `scale`
+ * Every tie goes to the lower index, and the order is that of the exact values:
+ * f32 results too close to tell apart are compared in f64.  A logit of -inf or
+ * NaN, or a bias of -inf or NaN, makes its expert unavailable (its p counts in
+ * the softmax only if its logit is usable); +inf reads as the largest f32.  A
+ * range short of available experts has the value -inf.  A slot for which no
+ * expert is left gets id -1 and weight 0.
+ *   logits   device, [T,experts], f32 or bf16 patterns (logits_bf16 != 0)
+ *   bias     device, f32 [experts], or NULL
+ *   ids      device, out: int32 [T,top_k];  weights  device, out: f32 [T,top_k]
+ * Errors: argument checks as above (T = 0 is a no-op); a score that is not of the
+ * enum, top_k outside 1..experts or above 32, group_top not 1 or 2 -> INVALID_ARG;
+ * experts above 1024, groups above 32 or not dividing experts, top_groups outside
+ * 1..groups, ranges smaller than group_top, or fewer than top_k experts in
+ * top_groups ranges -> QL_ERR_UNSUPPORTED_SHAPE. */
+typedef enum ql_route_score { QL_ROUTE_SOFTMAX = 0, QL_ROUTE_SIGMOID = 1 } ql_route_score;
+#define QL_ROUTE_MAX_EXPERTS 1024
+#define QL_ROUTE_MAX_TOP_K 32
+#define QL_ROUTE_MAX_GROUPS 32
+typedef struct ql_route_config {
+  int64_t experts;
+  int64_t top_k;
+  int64_t groups;      /* 1: no groups */
+  int64_t top_groups;
+  int64_t group_top;   /* 1 or 2 */
+  int32_t score;       /* ql_route_score */
+  int32_t renormalize;
+  float scale;
+} ql_route_config;
+ql_status qlinear_route(const void* logits, int logits_bf16, const ql_route_config* config, const float* bias,
+                        int64_t T, int32_t* ids, float* weights, void* stream);
+
+/* The routed tokens' products with their experts' 4-bit weights, W_e the e-th
+ * matrix of w and e = ids[t,j]:
+ *   weights NULL:  x [T,K],       y[t,j,:] = bf16_rne(W_e x[t])           [T,top_k,N]
+ *                  (the gate and up rows, before the activation)
+ *   weights given: x [T,top_k,K], y[t,:] = bf16_rne(sum_j weights[t,j] W_e x[t,j])  [T,N]
+ *                  (the down rows and the combination, summed in f32)
+ * Activations are not rounded and sums are f32, as in qlinear_forward_w4.  An id
+ * outside [0, experts) takes part in nothing: its rows of y are zero, or its term
+ * is left out.  A token may name an expert twice.
+ *   ids        device, int32 [T,top_k], as qlinear_route writes them
+ *   weights    device, f32 [T,top_k], or NULL
+ *   workspace  device, qlinear_experts_w4_workspace_bytes(T, top_k, w, weights !=
+ *              NULL) bytes, as for qlinear_forward_w4
+ * wq, sw and wz as in qlinear_forward_w4.  Errors: argument checks as above; T = 0
+ * is a no-op; top_k outside 1..32 -> INVALID_ARG; experts above 1024 ->
+ * QL_ERR_UNSUPPORTED_SHAPE; QL_ERR_WORKSPACE. */
+ql_status qlinear_experts_w4(const uint16_t* x, const int32_t* ids, const float* weights, const ql_w4_weight* w,
+                             int64_t T, int64_t top_k, uint16_t* y, void* workspace, size_t ws_bytes,
+                             void* stream);
+size_t qlinear_experts_w4_workspace_bytes(int64_t T, int64_t top_k, const ql_w4_weight* w, int combine);
+
 /* Test hook for the timeout path (no counterpart in the pages): qlinear_gemv
  * with its weight-copy engine held back, so that every consumer's bounded wait
  * runs out after about 2 s; the kernel records QL_ERR_TIMEOUT (detail: the
