@@ -621,7 +621,7 @@ ql_status check_w4_shape(const ql_w4_weight* w) {
   if (!w || w->N <= 0 || w->K <= 0 || w->experts <= 0) return QL_ERR_INVALID_ARG;
   if (w->group != 32 && w->group != 64 && w->group != 128) return QL_ERR_UNSUPPORTED_SHAPE;
   if (w->K % 32 || w->K >= kIndexLimit || w->N >= kIndexLimit || w->experts >= kIndexLimit ||
-      w->experts * w->N >= kIndexLimit)
+      w->experts * w->N > kIndexLimit - 512)
     return QL_ERR_UNSUPPORTED_SHAPE;
   return QL_OK;
 }
@@ -638,6 +638,12 @@ ql_status check_w4_experts(const ql_w4_weight* w, int64_t T, int64_t top_k) {
   if (T < 0 || top_k < 1 || top_k > QL_ROUTE_MAX_TOP_K) return QL_ERR_INVALID_ARG;
   if (w->experts > QL_ROUTE_MAX_EXPERTS || T >= kIndexLimit / QL_ROUTE_MAX_TOP_K) return QL_ERR_UNSUPPORTED_SHAPE;
   return QL_OK;
+}
+
+ql_status check_scratch(const void* workspace, size_t have, size_t want) {
+  if (!want) return QL_OK;
+  if (!workspace || have < want) return QL_ERR_WORKSPACE;
+  return (reinterpret_cast<uintptr_t>(workspace) & 255u) ? QL_ERR_MISALIGNED : QL_OK;
 }
 
 }  // namespace
@@ -659,9 +665,10 @@ ql_status qlinear_quantize_weight_w4(const uint16_t* w, int64_t N, int64_t K, in
 }
 
 size_t qlinear_forward_w4_workspace_bytes(int64_t M, const ql_w4_weight* w) {
-  (void)M;
-  (void)w;
-  return 0;
+  if (check_w4_shape(w) != QL_OK || M <= 0 || M >= kIndexLimit) return 0;
+  DeviceInfo d;
+  if (current_device(&d) != QL_OK) return 0;
+  return ql::w4_workspace_bytes(M, *w, d.sms);
 }
 
 ql_status qlinear_forward_w4(const uint16_t* x, const ql_w4_weight* w, int64_t M, uint16_t* y,
@@ -673,11 +680,10 @@ ql_status qlinear_forward_w4(const uint16_t* x, const ql_w4_weight* w, int64_t M
   QL_TRY(need(x));
   QL_TRY(check_w4_pointers(w));
   QL_TRY(need(y));
-  (void)workspace;
-  (void)ws_bytes;
   DeviceInfo d;
   QL_TRY(current_device(&d));
-  cudaError_t e = ql::launch_w4_stream(x, *w, M, y, static_cast<cudaStream_t>(stream));
+  QL_TRY(check_scratch(workspace, ws_bytes, ql::w4_workspace_bytes(M, *w, d.sms)));
+  cudaError_t e = ql::launch_w4(x, *w, M, y, workspace, d.sms, d.status, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? QL_OK : cuda_fail(e, "qlinear_forward_w4");
 }
 
@@ -705,11 +711,10 @@ ql_status qlinear_route(const void* logits, int logits_bf16, const ql_route_conf
 }
 
 size_t qlinear_experts_w4_workspace_bytes(int64_t T, int64_t top_k, const ql_w4_weight* w, int combine) {
-  (void)T;
-  (void)top_k;
-  (void)w;
-  (void)combine;
-  return 0;
+  if (check_w4_experts(w, T, top_k) != QL_OK || T == 0) return 0;
+  DeviceInfo d;
+  if (current_device(&d) != QL_OK) return 0;
+  return ql::w4_experts_workspace_bytes(T, top_k, *w, combine != 0, d.sms);
 }
 
 ql_status qlinear_experts_w4(const uint16_t* x, const int32_t* ids, const float* weights, const ql_w4_weight* w,
@@ -722,11 +727,11 @@ ql_status qlinear_experts_w4(const uint16_t* x, const int32_t* ids, const float*
   if (weights && !aligned16(weights)) return QL_ERR_MISALIGNED;
   QL_TRY(check_w4_pointers(w));
   QL_TRY(need(y));
-  (void)workspace;
-  (void)ws_bytes;
   DeviceInfo d;
   QL_TRY(current_device(&d));
-  cudaError_t e = ql::launch_w4_stream_experts(x, ids, weights, *w, T, top_k, y, static_cast<cudaStream_t>(stream));
+  QL_TRY(check_scratch(workspace, ws_bytes, ql::w4_experts_workspace_bytes(T, top_k, *w, weights != nullptr, d.sms)));
+  cudaError_t e = ql::launch_w4_experts(x, ids, weights, *w, T, top_k, y, workspace, d.sms, d.status,
+                                        static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? QL_OK : cuda_fail(e, "qlinear_experts_w4");
 }
 

@@ -125,6 +125,15 @@ cudaError_t launch_gemm_small(ql_scheme scheme, const uint16_t* x, const void* w
 cudaError_t launch_w4_stream(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint16_t* y, cudaStream_t st);
 cudaError_t launch_w4_stream_experts(const uint16_t* x, const int32_t* ids, const float* weights,
                                      const ql_w4_weight& w, int64_t T, int64_t topk, uint16_t* y, cudaStream_t st);
+// The product and the experts' products for any number of tokens: the kernels above
+// for few, tcgen05 for many.  workspace: *_workspace_bytes bytes of scratch.
+size_t w4_workspace_bytes(int64_t M, const ql_w4_weight& w, int sms);
+cudaError_t launch_w4(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint16_t* y, void* workspace, int sms,
+                      DevStatus* status, cudaStream_t st);
+size_t w4_experts_workspace_bytes(int64_t T, int64_t topk, const ql_w4_weight& w, bool combine, int sms);
+cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float* weights, const ql_w4_weight& w,
+                              int64_t T, int64_t topk, uint16_t* y, void* workspace, int sms, DevStatus* status,
+                              cudaStream_t st);
 cudaError_t launch_quantize_w4(const uint16_t* w, int64_t N, int64_t K, int64_t group, uint8_t* wq, uint16_t* sw,
                                uint8_t* wz, cudaStream_t st);
 cudaError_t launch_route(const void* logits, bool bf16, const ql_route_config& c, const float* bias, int64_t T,

@@ -60,5 +60,99 @@ QL_DEVINL void load_words(const uint8_t* p, uint32_t (&w)[kWords]) {
 
 QL_DEVINL void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
+// ---- f16 pairs of scaled weights (the tcgen05 path)
+QL_DEVINL uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+QL_DEVINL uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+QL_DEVINL uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+QL_DEVINL uint32_t f32x2_to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Eight codes -> four f16 pairs (q - z) s in the order of codes_to_bf16.  A nibble in
+// bits 0-3 of f16 1024.0 reads as 1024 + q, one in bits 4-7 as 1024 + 16 q, so one
+// shift serves four pairs; zlo = (1024 + z) twice, zhi = -(64 + z) twice.  q - z is
+// exact; times s it is exact for z = 8 (at most 3 + 8 significant bits), and rounded
+// to 11 bits otherwise.
+QL_DEVINL void codes_to_f16(uint32_t w, uint32_t zlo, uint32_t zhi, uint32_t s, uint32_t* p) {
+  constexpr uint32_t kSixteenth = 0x2C002C00u;
+  const uint32_t v = w >> 8;
+  p[0] = mul_f16x2(sub_f16x2(and_or<0x000F000Fu, 0x64006400u>(w), zlo), s);
+  p[1] = mul_f16x2(fma_f16x2(and_or<0x00F000F0u, 0x64006400u>(w), kSixteenth, zhi), s);
+  p[2] = mul_f16x2(sub_f16x2(and_or<0x000F000Fu, 0x64006400u>(v), zlo), s);
+  p[3] = mul_f16x2(fma_f16x2(and_or<0x00F000F0u, 0x64006400u>(v), kSixteenth, zhi), s);
+}
+
+// ---- tcgen05 with the A operand in TMEM
+// kind::f16 with f16 operands: the fields of tc::idesc_bf16 with A and B format 0.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, K = 16: A holds row i in lane i, two inputs to a column.
+QL_DEVINL void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(id), "r"(accumulate)
+      : "memory");
+}
+
+// Lane i of the warp stores its 32 registers to TMEM lane (taddr.lane + i), columns
+// [taddr.col, taddr.col + 32).
+QL_DEVINL void st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+QL_DEVINL void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 columns of one lane quarter.
+QL_DEVINL void ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Four rows of a row-major matrix by index, 128 bytes each from byte x, into 512
+// consecutive bytes (128-byte swizzle).  The map's box is one row high.
+QL_DEVINL void tma_gather4(void* dst, const CUtensorMap* map, int32_t x, int4 rows, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// ---- clusters
+QL_DEVINL void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+QL_DEVINL float ld_cluster(uint32_t saddr, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+      : "=f"(v)
+      : "r"(saddr), "r"(rank)
+      : "memory");
+  return v;
+}
+
 }  // namespace w4
 }  // namespace ql

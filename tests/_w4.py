@@ -23,20 +23,27 @@ def dequantize(wq, sw, wz, group):
     return (q - z).double() * sw[..., k // group].double()
 
 
-def product_limit(y, mag, K, roundings=1):
+def product_limit(y, mag, K, zeros=False):
     """Largest allowed |kernel - exact|: the output's bf16 rounding (half a step:
     2^-8 of the value), and f32 sums of exact products: K / 16 tensor-core steps
     and at most 64 further additions, each off by at most 2^-22 of the sum of the
-    magnitudes `mag` (a 17-term sum inside a step may truncate)."""
-    return roundings * 2.0 ** -8 * y.abs() + (K / 16 + 64) * 2.0 ** -22 * mag + 1e-38
+    magnitudes `mag` (a 17-term sum inside a step may truncate).
+
+    With zero points a weight may be rounded once: q - z is an integer of up to 4
+    bits (|q - z| <= 15), s has 8 significant bits, their product up to 12, and f16,
+    in which the tensor cores take it, 11.  That rounding is off by at most half a
+    step, 2^-11 of the weight, so by 2^-11 of |x w| in each term and 2^-11 `mag` in
+    the sum.  (For z = 8, |q - z| <= 8 has at most 3 significant bits, the product
+    11: exact.)"""
+    return 2.0 ** -8 * y.abs() + ((K / 16 + 64) * 2.0 ** -22 + (2.0 ** -11 if zeros else 0.0)) * mag + 1e-38
 
 
-def assert_product(got, x, w, roundings=1, what=""):
+def assert_product(got, x, w, zeros=False, what=""):
     """got bf16 [M,N] against x [M,K] @ w[N,K]^T in float64."""
     y = x.double() @ w.t()
     mag = x.double().abs() @ w.abs().t()
     err = (got.double().cpu() - y).abs()
-    lim = product_limit(y, mag, w.shape[1], roundings)
+    lim = product_limit(y, mag, w.shape[1], zeros)
     bad = (~(err <= lim)).nonzero()
     assert bad.numel() == 0, (what, bad.shape[0], [(tuple(b.tolist()), got.double().cpu()[tuple(b)].item(),
                                                     y[tuple(b)].item(), lim[tuple(b)].item()) for b in bad[:4]])

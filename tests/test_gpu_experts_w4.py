@@ -37,7 +37,7 @@ def _check(x, ids, wq, sw, wz, wts, group):
     assert ql.device_status()[0] == 0
     assert buf[:256].isnan().all() and buf[256 + n:].isnan().all()
     ref, mag = _w4.experts64(x, ids, _w4.dequantize(wq, sw, wz, group), wts)
-    lim = _w4.product_limit(ref, mag, x.shape[-1])
+    lim = _w4.product_limit(ref, mag, x.shape[-1], wz is not None)
     if combine:
         # sum_j |w_j| |y_j| <= the magnitude, but a bf16 rounding is relative to each
         # pair's own value: bound it by the pairs' values
@@ -129,7 +129,7 @@ def test_route_up_activation_down(cuda, T):
         assert ((h.double() - ref).abs() <= _w4.product_limit(ref, mag, H)).all()
         ref, mag = _w4.experts64(act, ids, wd, wts)
         pairs, _ = _w4.experts64(act.reshape(T * k, I), ids.reshape(T * k, 1), wd)
-        lim = _w4.product_limit(ref, mag, I) + 2.0 ** -8 * (pairs.view(T, k, H).abs() * wts.double()[..., None]).sum(1)
+        lim = _w4.product_limit(ref, mag, I, True) + 2.0 ** -8 * (pairs.view(T, k, H).abs() * wts.double()[..., None]).sum(1)
         assert ((y.double() - ref).abs() <= lim).all()
 
     verify(_layer(ld, xd, up, down, k, E, ws_up, ws_down), x, logits)

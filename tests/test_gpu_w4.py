@@ -37,7 +37,7 @@ def _check(x, wq, sw, wz, group, what=""):
     out = ql.forward_w4(x.cuda(), _handle(wq, sw, wz, group), y=y)
     assert out is y and ql.device_status()[0] == 0
     assert buf[:256].isnan().all() and buf[256 + M * N:].isnan().all()
-    _w4.assert_product(y, x, _w4.dequantize(wq, sw, wz, group), what=what)
+    _w4.assert_product(y, x, _w4.dequantize(wq, sw, wz, group), wz is not None, what)
     return y
 
 
@@ -135,7 +135,7 @@ def test_side_stream_and_graph(cuda, M):
         d.copy_(h)
     graph.replay()
     torch.cuda.synchronize()
-    _w4.assert_product(out, x2, _w4.dequantize(wq2, sw2, wz2, 64))
+    _w4.assert_product(out, x2, _w4.dequantize(wq2, sw2, wz2, 64), True)
 
 
 @pytest.mark.parametrize("M", [1, 40])
