@@ -130,6 +130,10 @@ QL_DEVINL void ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+QL_DEVINL void ld1(uint32_t taddr, uint32_t (&r)[1]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr));
+}
+
 // Four rows of a row-major matrix by index, 128 bytes each from byte x, into 512
 // consecutive bytes (128-byte swizzle).  The map's box is one row high.
 QL_DEVINL void tma_gather4(void* dst, const CUtensorMap* map, int32_t x, int4 rows, uint64_t* bar) {

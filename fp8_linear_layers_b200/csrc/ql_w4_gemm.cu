@@ -36,7 +36,7 @@ constexpr int kG4StageK = 256;   // inputs of a weight stage (128 bytes of codes
 constexpr int kG4GranK = 64;     // inputs of a token stage and of a TMEM weight slot
 constexpr int kG4WStages = 3;
 constexpr int kG4Slots = 4;      // TMEM weight slots of 32 columns, over all row tiles
-constexpr int kG4MaxTiles = 192; // tokens a tile can hold
+constexpr int kG4MaxXStages = 8;
 constexpr int kG4PrepThreads = 128;
 constexpr int kG4PlanThreads = 1024;
 constexpr int kG4MaxSplit = 8;
@@ -45,7 +45,7 @@ constexpr int kG4MaxSplit = 8;
 template <int RT>
 struct G4Cfg {
   static constexpr int kTok = RT == 2 ? 192 : 128;  // largest token tile
-  static constexpr int kXStages = 4;
+  static constexpr int kRing = RT == 2 ? 110592 : 57344;  // bytes of token stages, 3 to 8 of them
   static constexpr int kTmem = RT == 2 ? 512 : 256;
   static constexpr int kDCols = RT == 2 ? 192 : 128;  // columns of one accumulator
   static constexpr int kWBytes = RT * 128 * 128;
@@ -68,6 +68,7 @@ struct G4Params {
   int groups;
   int ntok;              // tokens of a tile (a multiple of 16)
   int xstage;            // bytes of a token stage
+  int xstages;           // token stages
   int rows_per_token;    // experts: pairs that share an x row (topk for gather, else 1)
   int splits;            // CTAs of a cluster along K
   DevStatus* status;
@@ -86,23 +87,25 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
     w4_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const G4Params p) {
   using Cfg = G4Cfg<RT>;
-  constexpr int kXS = Cfg::kXStages;
+  const int xs_n = p.xstages;
   constexpr int kPerStage = kG4StageK / kGroup;  // scales of a row in a weight stage
   extern __shared__ uint8_t smem_raw[];
   uint8_t* wring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* xring = wring + kG4WStages * Cfg::kWBytes;
-  uint64_t* wfull = reinterpret_cast<uint64_t*>(xring + kXS * p.xstage);
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(xring + xs_n * p.xstage);
   uint64_t* wempty = wfull + kG4WStages;
   uint64_t* xfull = wempty + kG4WStages;
-  uint64_t* xempty = xfull + kXS;
-  uint64_t* afull = xempty + kXS;
+  uint64_t* xempty = xfull + kG4MaxXStages;
+  uint64_t* afull = xempty + kG4MaxXStages;
   uint64_t* aempty = afull + kG4Slots;
   uint64_t* done = aempty + kG4Slots;
-  int* s_ex = reinterpret_cast<int*>(done + 2);    // [kTok] the columns' exponents (16-byte aligned)
+  int* s_ex = reinterpret_cast<int*>(done + 2);     // [kTok] the columns' exponents (16-byte aligned)
   int* s_row = s_ex + Cfg::kTok;                    // [kTok] experts: x rows
   int* s_out = s_row + Cfg::kTok;                   // [kTok] experts: pairs
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_out + Cfg::kTok);
+  float* s_fac = reinterpret_cast<float*>(s_out + Cfg::kTok);  // [kTok] 2^-exponent
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_fac + Cfg::kTok);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* s_wide = reinterpret_cast<int*>(tmem_holder + 2);  // an exponent that one factor cannot take
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % p.splits;
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
       mbar_init(&wfull[s], 1);
       mbar_init(&wempty[s], kG4DequantWarps);
     }
-    for (int s = 0; s < kXS; ++s) {
+    for (int s = 0; s < xs_n; ++s) {
       mbar_init(&xfull[s], 1);
       mbar_init(&xempty[s], 1);
     }
@@ -127,6 +130,7 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
     }
     mbar_init(done, 1);
     *abort_flag = 0;
+    *s_wide = 0;
     fence_barrier_init();
     tc::prefetch_tmap(&tmW);
     tc::prefetch_tmap(&tmX);
@@ -135,10 +139,11 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
     tc::tmem_alloc(tmem_holder, Cfg::kTmem);
     tc::tmem_relinquish();
   }
+  __syncthreads();
   tc::grid_dependency_wait();  // the prepare kernel's tokens, pairs and tiles
   tc::launch_dependents();
 
-  // this CTA's tokens
+  // this CTA's tokens: exponent, and as a factor 2^-ex
   int64_t e = 0, m0 = 0;
   int count;
   if constexpr (kExperts) {
@@ -149,14 +154,22 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
     for (int i = threadIdx.x; i < p.ntok && count > 0; i += kG4Threads) {
       const int pair = p.order[tile.start + min(i, count - 1)];
       const int row = pair / p.rows_per_token;
+      const int ex = p.ex[row];
       s_out[i] = pair;
       s_row[i] = row;
-      s_ex[i] = p.ex[row];
+      s_ex[i] = ex;
+      s_fac[i] = exp2i(max(-126, min(126, -ex)));
+      if (abs(ex) > 60) *s_wide = 1;
     }
   } else {
     m0 = (int64_t)blockIdx.y * p.ntok;
     count = (int)min((int64_t)p.ntok, p.M - m0);
-    for (int i = threadIdx.x; i < count; i += kG4Threads) s_ex[i] = p.ex[m0 + i];
+    for (int i = threadIdx.x; i < count; i += kG4Threads) {
+      const int ex = p.ex[m0 + i];
+      s_ex[i] = ex;
+      s_fac[i] = exp2i(max(-126, min(126, -ex)));
+      if (abs(ex) > 60) *s_wide = 1;
+    }
   }
   tc::fence_before();
   __syncthreads();
@@ -174,20 +187,21 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
       const uint32_t xbytes = kExperts ? (uint32_t)((count + 3) / 4) * 512u : (uint32_t)p.ntok * 128u;
       bool ok = true;
       int jw = 0, jx = 0;  // issued stages
+      int s = 0;           // token stage of granule j, and how often it was filled
+      uint32_t fill = 0;
       for (int j = 0; j < ngran && ok; ++j) {
         if (j % 4 == 0) {
-          const int s = jw % kG4WStages;
-          if (jw >= kG4WStages) ok = mbar_wait_bounded(&wempty[s], ((jw / kG4WStages) - 1) & 1, abort_flag);
+          const int v = jw % kG4WStages;
+          if (jw >= kG4WStages) ok = mbar_wait_bounded(&wempty[v], ((jw / kG4WStages) - 1) & 1, abort_flag);
           if (!ok) break;
-          mbar_arrive_expect_tx(&wfull[s], Cfg::kWBytes);
+          mbar_arrive_expect_tx(&wfull[v], Cfg::kWBytes);
 #pragma unroll
           for (int r = 0; r < RT; ++r)
-            tc::tma_load_2d(wring + s * Cfg::kWBytes + r * 16384, &tmW, (w0 + jw) * 128, wrow + r * 128, &wfull[s],
+            tc::tma_load_2d(wring + v * Cfg::kWBytes + r * 16384, &tmW, (w0 + jw) * 128, wrow + r * 128, &wfull[v],
                             pol_w);
           ++jw;
         }
-        const int s = j % kXS;
-        if (j >= kXS) ok = mbar_wait_bounded(&xempty[s], ((j / kXS) - 1) & 1, abort_flag);
+        if (fill > 0) ok = mbar_wait_bounded(&xempty[s], (fill - 1) & 1, abort_flag);
         if (!ok) break;
         mbar_arrive_expect_tx(&xfull[s], xbytes);
         uint8_t* dst = xring + s * p.xstage;
@@ -199,6 +213,10 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
           tc::tma_load_2d(dst, &tmX, xb, (int)m0, &xfull[s], pol_x);
         }
         ++jx;
+        if (++s == xs_n) {
+          s = 0;
+          ++fill;
+        }
       }
       if (!ok) {
         if (!*abort_flag) record_timeout(p.status, KID_W4, 1);
@@ -206,7 +224,7 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
         // the copies in flight land before the CTA leaves
         for (int j = max(0, jw - kG4WStages); j < jw; ++j)
           mbar_wait_bounded(&wfull[j % kG4WStages], (j / kG4WStages) & 1, nullptr);
-        for (int j = max(0, jx - kXS); j < jx; ++j) mbar_wait_bounded(&xfull[j % kXS], (j / kXS) & 1, nullptr);
+        for (int j = max(0, jx - xs_n); j < jx; ++j) mbar_wait_bounded(&xfull[j % xs_n], (j / xs_n) & 1, nullptr);
       }
     }
   } else if (count > 0 && warp == kG4MmaWarp) {
@@ -214,9 +232,10 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
     if (lane == 0) {
       const uint32_t id = w4::idesc_f16(128, mma_n);
       bool ok = true;
+      int xs = 0;
+      uint32_t xphase = 0;
       for (int j = 0; j < ngran && ok; ++j) {
-        const int xs = j % kXS;
-        ok = mbar_wait_bounded(&xfull[xs], (j / kXS) & 1, abort_flag);
+        ok = mbar_wait_bounded(&xfull[xs], xphase, abort_flag);
         const uint64_t bdesc = tc::sw128_desc(smem_u32(xring + xs * p.xstage));
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -231,6 +250,10 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
           tc::commit(&aempty[slot]);
         }
         if (ok) tc::commit(&xempty[xs]);
+        if (++xs == xs_n) {
+          xs = 0;
+          xphase ^= 1;
+        }
       }
       if (!ok) {
         if (!*abort_flag) record_timeout(p.status, KID_W4, 2);
@@ -341,23 +364,44 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       tc::fence_after();
-      float* part = reinterpret_cast<float*>(wring);  // split K: [ntok][128 RT] partial sums
+      // Staged in the rings, which every MMA has left behind: split K, [tok][128 RT]
+      // partial sums; else [tok][128 RT] bf16 (rows padded by 16 bytes), so that the
+      // rows leave in 16-byte stores, 512 or 256 bytes of a token together.
+      constexpr int kRow = RT * 128 * 2 + 16;
+      float* part = reinterpret_cast<float*>(wring);
+      const int col = r * 128 + q * 32 + lane;
       const int half = ((mma_n / 16 + 1) / 2) * 16;
       const int c_lo = RT == 2 ? 0 : wg ? half : 0, c_hi = RT == 2 ? mma_n : wg ? mma_n : half;
+      const bool wide = __any_sync(0xffffffffu, *s_wide || abs(f) > 60);
+      const float rf = exp2i(max(-126, min(126, -f)));
       for (int c = c_lo; c < c_hi; c += 16) {
         uint32_t v[16];
         w4::ld16(tmem + r * Cfg::kDCols + lane_addr + c, v);
         tc::ld_wait();
+        float o[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (c + i >= count) break;
-          const float out = scale2(__uint_as_float(v[i]), -(f + s_ex[c + i]));
-          if (p.splits > 1) {
-            part[(c + i) * (RT * 128) + r * 128 + q * 32 + lane] = out;
-          } else if (n < p.N) {
-            const int64_t row = kExperts ? s_out[c + i] : m0 + c + i;
-            p.y[row * p.N + n] = f32_to_bf16_rn(out);
-          }
+        for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(v[i]) * rf * s_fac[c + i];
+        if (wide) {  // the two factors together may leave f32's range where their product does not
+#pragma unroll 1
+          for (int i = 0; i < 16; ++i)
+            if (c + i < count) {
+              uint32_t one[1];
+              w4::ld1(tmem + r * Cfg::kDCols + lane_addr + c + i, one);
+              tc::ld_wait();
+              const float t = scale2(__uint_as_float(one[0]), -(f + s_ex[c + i]));
+              if (p.splits > 1)
+                part[(c + i) * (RT * 128) + col] = t;
+              else
+                *reinterpret_cast<uint16_t*>(wring + (c + i) * kRow + col * 2) = f32_to_bf16_rn(t);
+            }
+        } else if (p.splits > 1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c + i < count) part[(c + i) * (RT * 128) + col] = o[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c + i < count) *reinterpret_cast<uint16_t*>(wring + (c + i) * kRow + col * 2) = f32_to_bf16_rn(o[i]);
         }
       }
       tc::fence_before();
@@ -368,6 +412,10 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
   if (p.splits > 1) {
     // the cluster's partial sums, added in the order of their K ranges
     w4::cluster_sync();
+    if (warp == kG4MmaWarp) {
+      tc::fence_after();
+      tc::tmem_dealloc(tmem, Cfg::kTmem);
+    }
     if (!*abort_flag) {
       const uint32_t part = smem_u32(wring);
       for (int i = threadIdx.x; i < RT * 128 * ((count - split + p.splits - 1) / p.splits); i += kG4Threads) {
@@ -379,13 +427,36 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
         p.y[(m0 + c) * p.N + n0 + col] = f32_to_bf16_rn(sum);
       }
     }
+    __syncwarp();
     w4::cluster_sync();  // no CTA leaves while another reads its sums
   } else {
     __syncthreads();
-  }
-  if (warp == kG4MmaWarp) {
-    tc::fence_after();
-    tc::tmem_dealloc(tmem, Cfg::kTmem);
+    // before the copies below, in which a warp's lanes may part: dealloc is a
+    // whole-warp instruction
+    if (warp == kG4MmaWarp) {
+      tc::fence_after();
+      tc::tmem_dealloc(tmem, Cfg::kTmem);
+    }
+    if (count > 0 && !*abort_flag) {
+      constexpr int kRow = RT * 128 * 2 + 16;
+      constexpr int kVecs = RT * 16;  // 16-byte pieces of a token's row
+      const int cols = (int)min((int64_t)(RT * 128), p.N - n0);
+      if ((p.N & 7) == 0) {
+        for (int i = threadIdx.x; i < count * kVecs; i += kG4Threads) {
+          const int c = i / kVecs, b = i % kVecs;
+          const int64_t row = kExperts ? s_out[c] : m0 + c;
+          if (b * 8 < cols)
+            *reinterpret_cast<uint4*>(p.y + row * p.N + n0 + b * 8) =
+                *reinterpret_cast<const uint4*>(wring + c * kRow + b * 16);
+        }
+      } else {
+        for (int i = threadIdx.x; i < count * RT * 128; i += kG4Threads) {
+          const int c = i / (RT * 128), b = i % (RT * 128);
+          const int64_t row = kExperts ? s_out[c] : m0 + c;
+          if (b < cols) p.y[row * p.N + n0 + b] = *reinterpret_cast<const uint16_t*>(wring + c * kRow + b * 2);
+        }
+      }
+    }
   }
 }
 
@@ -641,8 +712,8 @@ template <int RT, int kGroup, bool kZero, bool kExperts>
 cudaError_t launch_g4_t(const CUtensorMap& tw, const CUtensorMap& tx, const G4Params& p, const G4Plan& g,
                         cudaStream_t st) {
   using Cfg = G4Cfg<RT>;
-  const int smem = 1024 + kG4WStages * Cfg::kWBytes + Cfg::kXStages * p.xstage +
-                   8 * (2 * kG4WStages + 2 * Cfg::kXStages + 2 * kG4Slots + 2) + 12 * Cfg::kTok + 16;
+  const int smem = 1024 + kG4WStages * Cfg::kWBytes + p.xstages * p.xstage +
+                   8 * (2 * kG4WStages + 2 * kG4MaxXStages + 2 * kG4Slots + 2) + 16 * Cfg::kTok + 16;
   cudaError_t e = ensure_smem<w4_gemm_kernel<RT, kGroup, kZero, kExperts>>(smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -692,6 +763,7 @@ cudaError_t launch_g4(const ql_w4_weight& w, const uint16_t* x16, int64_t rows, 
   p.ntok = g.ntok;
   p.xstage = (int)div_up(g.ntok * 128, 1024) * 1024;
   p.splits = g.splits;
+  p.xstages = std::min(kG4MaxXStages, std::max(3, (g.rt == 2 ? G4Cfg<2>::kRing : G4Cfg<1>::kRing) / p.xstage));
   return g.rt == 2 ? launch_g4_group<2, kExperts>(tw, tx, p, g, (int)w.group, st)
                    : launch_g4_group<1, kExperts>(tw, tx, p, g, (int)w.group, st);
 }

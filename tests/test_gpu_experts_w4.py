@@ -75,6 +75,17 @@ def test_uneven_ids(cuda, combine, T, kind):
         assert not y.any()
 
 
+@pytest.mark.parametrize("combine", [False, True])
+@pytest.mark.parametrize("N", [40, 41])
+@pytest.mark.parametrize("counts", [(19,), (39, 1), (18, 33, 3), (1, 2, 31, 32, 64, 5), (17,) * 6, (59, 21)])
+def test_pairs_of_an_expert(cuda, combine, N, counts):
+    """Experts with one, an odd number of, and more pairs than a token tile holds."""
+    x, ids, wq, sw, wz, wts = _case(sum(counts), 1, 24, N, 128, 64, False, combine)
+    ids[:, 0] = torch.repeat_interleave(torch.arange(len(counts)) * 3, torch.tensor(counts)).int()
+    ids = ids[torch.randperm(len(ids), generator=_gen(1))].contiguous()
+    _check(x, ids, wq, sw, wz, wts, 64)
+
+
 @pytest.mark.parametrize("T", [2, 40])
 def test_non_finite_stays_with_its_token(cuda, T):
     """An infinite token, or an expert with an infinite scale, touches no other row."""
