@@ -96,18 +96,52 @@ QL_DEVINL void codes_to_f16(uint32_t w, uint32_t zlo, uint32_t zhi, uint32_t s, 
   p[3] = mul_f16x2(fma_f16x2(and_or<0x00F000F0u, 0x64006400u>(v), kSixteenth, zhi), s);
 }
 
+// mbar_wait_bounded for a whole warp, whose lanes arrive together.  It polls every few
+// dozen cycles before the bounded wait, whose timer costs 700 cycles to start, takes over.
+QL_DEVINL bool wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  bool ok = mbar_try_wait(a, parity);
+#pragma unroll 1
+  for (int i = 0; i < 4096 && !__all_sync(0xffffffffu, ok); ++i) {
+    __nanosleep(20);
+    ok = mbar_try_wait(a, parity);
+  }
+  if (!__all_sync(0xffffffffu, ok)) ok = mbar_wait_bounded(bar, parity, abort);
+  return __all_sync(0xffffffffu, ok);
+}
+
 // ---- tcgen05 with the A operand in TMEM
 // kind::f16 with f16 operands: the fields of tc::idesc_bf16 with A and B format 0.
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, K = 16: A holds row i in lane i, two inputs to a column.
-QL_DEVINL void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t id, uint32_t accumulate) {
+// One lane of a converged warp (the same one each time).
+QL_DEVINL uint32_t elect_one() {
+  uint32_t pred;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(id), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(pred));
+  return pred;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, K = 16: A holds row i in lane i, two inputs to a
+// column.  Called by the whole warp, issued by its elected lane: the operands are then
+// warp-uniform and live in uniform registers.  Inside a one-lane branch each issue
+// took 60 to 80 cycles to move them there, more than the MMA itself up to 128 tokens.
+QL_DEVINL void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t id, uint32_t accumulate,
+                          uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(id), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+QL_DEVINL void commit(uint64_t* bar, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(elected)
       : "memory");
 }
 
@@ -136,11 +170,13 @@ QL_DEVINL void ld1(uint32_t taddr, uint32_t (&r)[1]) {
 
 // Four rows of a row-major matrix by index, 128 bytes each from byte x, into 512
 // consecutive bytes (128-byte swizzle).  The map's box is one row high.
-QL_DEVINL void tma_gather4(void* dst, const CUtensorMap* map, int32_t x, int4 rows, uint64_t* bar) {
+QL_DEVINL void tma_gather4(uint32_t dst, const CUtensorMap* map, int32_t x, int4 rows, uint32_t bar,
+                           uint32_t elected) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(smem_u32(bar))
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %8, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(dst),
+      "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar), "r"(elected)
       : "memory");
 }
 

@@ -29,27 +29,33 @@ namespace ql {
 constexpr unsigned int KID_W4 = 4;  // KernelId of this file's GEMM in the device status word
 
 constexpr int kG4DequantWarps = 8;
-constexpr int kG4TmaWarp = 8;
-constexpr int kG4MmaWarp = 9;
-constexpr int kG4Threads = 320;
+constexpr int kG4Producers = 3;  // warps that issue the token loads of experts (dense: one)
 constexpr int kG4StageK = 256;   // inputs of a weight stage (128 bytes of codes a row)
 constexpr int kG4GranK = 64;     // inputs of a token stage and of a TMEM weight slot
 constexpr int kG4WStages = 3;
-constexpr int kG4Slots = 4;      // TMEM weight slots of 32 columns, over all row tiles
 constexpr int kG4MaxXStages = 8;
 constexpr int kG4PrepThreads = 128;
 constexpr int kG4PlanThreads = 1024;
 constexpr int kG4MaxSplit = 8;
 
-// RT 128-row weight tiles share the CTA's tokens.
-template <int RT>
-struct G4Cfg {
-  static constexpr int kTok = RT == 2 ? 192 : 128;  // largest token tile
-  static constexpr int kRing = RT == 2 ? 110592 : 57344;  // bytes of token stages, 3 to 8 of them
-  static constexpr int kTmem = RT == 2 ? 512 : 256;
-  static constexpr int kDCols = RT == 2 ? 192 : 128;  // columns of one accumulator
-  static constexpr int kWBytes = RT * 128 * 128;
-};
+// Wide kernel: two 128-row weight tiles share up to 192 tokens; one CTA to an SM, which
+// takes tile after tile.  TMEM: 2 x 192 accumulator columns, 2 slots x 2 tiles x 32.
+constexpr int kWideTok = 192;
+constexpr int kWideRing = 110592;  // bytes of token stages
+constexpr int kWideFirstProducer = kG4DequantWarps;
+constexpr int kWideMma = kWideFirstProducer + kG4Producers;
+constexpr int kWideFirstEpi = kWideMma + 1;
+constexpr int kWideEpiWarps = 8;
+constexpr int kWideThreads = (kWideFirstEpi + kWideEpiWarps) * 32;
+constexpr int kWideStageRow = 80;  // bytes of a token in an epilogue warp's staging (32 outputs and a pad)
+constexpr int kWideWBytes = 2 * 128 * 128;
+
+// Narrow kernel: one weight tile, up to 128 tokens, K split over a cluster; two CTAs to
+// an SM.  TMEM: 128 accumulator columns, 4 slots x 32.
+constexpr int kNarrowTok = 128;
+constexpr int kNarrowRing = 57344;
+constexpr int kNarrowSlots = 4;
+constexpr int kNarrowWBytes = 128 * 128;
 
 struct G4Tile {
   int expert, start, count, pad;
@@ -67,6 +73,7 @@ struct G4Params {
   int64_t M;             // dense: tokens
   int groups;
   int ntok;              // tokens of a tile (a multiple of 16)
+  int row_tiles, tok_tiles;  // wide, dense
   int xstage;            // bytes of a token stage
   int xstages;           // token stages
   int rows_per_token;    // experts: pairs that share an x row (topk for gather, else 1)
@@ -82,38 +89,145 @@ QL_DEVINL float scale2(float v, int e) {  // v 2^e, e in [-298, 254]
   return v * exp2i(h) * exp2i(e - h);
 }
 
-template <int RT, int kGroup, bool kZero, bool kExperts>
-__global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
-    w4_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                   const G4Params p) {
-  using Cfg = G4Cfg<RT>;
+// Position of the largest set exponent of a bf16 magnitude (floor of its log2); 0 -> zero.
+QL_DEVINL int log2_bf16(uint32_t mag, int zero) {
+  return mag >= 0x80u ? (int)(mag >> 7) - 127 : mag ? -133 + (31 - __clz(mag)) : zero;
+}
+
+// The power of two f that brings a row's largest |s| over groups [g0, g1) to [2^10, 2^11).
+QL_DEVINL int row_exponent(const uint16_t* sw, int g0, int g1, bool vec) {
+  uint32_t top = 0;
+  if (vec) {  // whole 16-byte pieces; a neighbour's scales do no harm beyond range
+    const uint4* v4 = reinterpret_cast<const uint4*>(sw);
+#pragma unroll 4
+    for (int i = g0 >> 3; i < (g1 + 7) >> 3; ++i) {
+      const uint4 v = __ldg(v4 + i);
+      top = max(max(max(top, v.x & 0x7FFFu), max(v.x >> 16 & 0x7FFFu, v.y & 0x7FFFu)),
+                max(max(v.y >> 16 & 0x7FFFu, v.z & 0x7FFFu),
+                    max(v.z >> 16 & 0x7FFFu, max(v.w & 0x7FFFu, v.w >> 16 & 0x7FFFu))));
+    }
+  } else {
+#pragma unroll 8
+    for (int i = g0; i < g1; ++i) top = max(top, (uint32_t)__ldg(sw + i) & 0x7FFFu);
+  }
+  return 10 - log2_bf16(min(top, 0x7F7Fu), 10);
+}
+
+// A row's scales and zero points of one weight stage, loaded a stage ahead.
+template <int kGroup, bool kZero>
+struct G4Scales {
+  static constexpr int kN = kG4StageK / kGroup;
+  uint32_t sraw[kN], zraw[kZero ? kN : 1];
+  uint32_t s2[kN], zl[kZero ? kN : 1], zh[kZero ? kN : 1];
+
+  QL_DEVINL void load(const uint16_t* sw, const uint8_t* wz, int w, int groups) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int gi = w * kN + i;
+      sraw[i] = gi < groups ? __ldg(sw + gi) : 0;
+      if constexpr (kZero) zraw[i] = gi < groups ? __ldg(wz + gi) : 8;
+    }
+  }
+  QL_DEVINL void convert(int f) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const float s = scale2(__uint_as_float(sraw[i] << 16), f);
+      s2[i] = w4::f32x2_to_f16x2(s, s);
+      if constexpr (kZero) {
+        zl[i] = 0x64006400u + zraw[i] * 0x10001u;
+        const float zf = -(64.0f + (float)zraw[i]);
+        zh[i] = w4::f32x2_to_f16x2(zf, zf);
+      }
+    }
+  }
+  // 64 inputs, granule gq of the stage, from this row's 128 swizzled bytes.
+  QL_DEVINL void granule(const uint8_t* row, int gq, uint32_t rsw, uint32_t (&h)[32]) const {
+    const uint4 c0 = *reinterpret_cast<const uint4*>(row + (((uint32_t)(2 * gq) ^ rsw) << 4));
+    const uint4 c1 = *reinterpret_cast<const uint4*>(row + (((uint32_t)(2 * gq + 1) ^ rsw) << 4));
+    const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int gi = (gq * 64 + i * 8) / kGroup;
+      if constexpr (kZero)
+        w4::codes_to_f16(c[i], zl[gi], zh[gi], s2[gi], h + 4 * i);
+      else
+        w4::codes_to_f16(c[i], 0x64086408u, 0xD480D480u, s2[gi], h + 4 * i);  // 1032, -72
+    }
+  }
+};
+
+// One granule of tokens to a stage: dense, a box of the token matrix; experts, this
+// producer warp's share of the gathered rows.
+template <bool kExperts>
+QL_DEVINL void load_tokens(const CUtensorMap& tmX, uint8_t* dst, uint64_t* bar, uint32_t bytes, int xb, int m0,
+                           const int* rows, int count, int pw, int lane, uint64_t policy) {
+  if constexpr (kExperts) {
+    if (pw == 0 && lane == 0) mbar_arrive_expect_tx(bar, bytes);
+    __syncwarp();
+    const uint32_t elected = w4::elect_one();
+    const uint32_t d = smem_u32(dst), b = smem_u32(bar);
+    for (int i = 4 * pw; i < count; i += 4 * kG4Producers)
+      w4::tma_gather4(d + i * 128, &tmX, xb, *reinterpret_cast<const int4*>(rows + i), b, elected);
+  } else {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, bytes);
+      tc::tma_load_2d(dst, &tmX, xb, m0, bar, policy);
+    }
+  }
+  __syncwarp();
+}
+
+// What the K range of a CTA looks like: weight stages [w0, w0 + n), taken in rotated
+// order.  The CTAs start at different stages: marching through K together they would
+// all read the same few token lines of L2 at a time.
+struct G4Range {
+  int w0, n, rot, nk64;
+  QL_DEVINL int stage(int j) const {
+    const int w = j + rot;
+    return w0 + (w < n ? w : w - n);
+  }
+  QL_DEVINL int granules(int w) const { return min(4, nk64 - w * 4); }
+  QL_DEVINL int total() const { return min((w0 + n) * 4, nk64) - w0 * 4; }
+};
+
+// ---------------------------------------------------------------------------- narrow
+
+template <int kGroup, bool kZero, bool kExperts>
+__global__ void __launch_bounds__((kG4DequantWarps + (kExperts ? kG4Producers : 1) + 1) * 32, 2)
+    w4_narrow_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                     const G4Params p) {
+  constexpr int kProducers = kExperts ? kG4Producers : 1;
+  constexpr int kMmaWarp = kG4DequantWarps + kProducers;
+  constexpr int kThreads = (kMmaWarp + 1) * 32;
+  constexpr int kSlots = kNarrowSlots;
   const int xs_n = p.xstages;
-  constexpr int kPerStage = kG4StageK / kGroup;  // scales of a row in a weight stage
   extern __shared__ uint8_t smem_raw[];
   uint8_t* wring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* xring = wring + kG4WStages * Cfg::kWBytes;
+  uint8_t* xring = wring + kG4WStages * kNarrowWBytes;
   uint64_t* wfull = reinterpret_cast<uint64_t*>(xring + xs_n * p.xstage);
   uint64_t* wempty = wfull + kG4WStages;
   uint64_t* xfull = wempty + kG4WStages;
   uint64_t* xempty = xfull + kG4MaxXStages;
   uint64_t* afull = xempty + kG4MaxXStages;
-  uint64_t* aempty = afull + kG4Slots;
-  uint64_t* done = aempty + kG4Slots;
-  int* s_ex = reinterpret_cast<int*>(done + 2);     // [kTok] the columns' exponents (16-byte aligned)
-  int* s_row = s_ex + Cfg::kTok;                    // [kTok] experts: x rows
-  int* s_out = s_row + Cfg::kTok;                   // [kTok] experts: pairs
-  float* s_fac = reinterpret_cast<float*>(s_out + Cfg::kTok);  // [kTok] 2^-exponent
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_fac + Cfg::kTok);
+  uint64_t* aempty = afull + kSlots;
+  uint64_t* done = aempty + kSlots;
+  int* s_ex = reinterpret_cast<int*>(done + 2);               // the columns' exponents (16-byte aligned)
+  int* s_row = s_ex + kNarrowTok;                              // experts: x rows
+  int* s_out = s_row + kNarrowTok;                             // experts: pairs
+  float* s_fac = reinterpret_cast<float*>(s_out + kNarrowTok); // 2^-exponent
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_fac + kNarrowTok);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_wide = reinterpret_cast<int*>(tmem_holder + 2);  // an exponent that one factor cannot take
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % p.splits;
-  const int64_t n0 = (int64_t)(blockIdx.x / p.splits) * (RT * 128);
-  const int nk64 = (int)((p.K + kG4GranK - 1) / kG4GranK);
+  const int64_t n0 = (int64_t)(blockIdx.x / p.splits) * 128;
   const int nkw = (int)((p.K + kG4StageK - 1) / kG4StageK);
-  const int w0 = (int)((int64_t)split * nkw / p.splits), w1 = (int)((int64_t)(split + 1) * nkw / p.splits);
-  const int ngran = min(w1 * 4, nk64) - w0 * 4;  // this CTA's granules
+  G4Range kr;
+  kr.nk64 = (int)((p.K + kG4GranK - 1) / kG4GranK);
+  kr.w0 = (int)((int64_t)split * nkw / p.splits);
+  kr.n = (int)((int64_t)(split + 1) * nkw / p.splits) - kr.w0;
+  kr.rot = (int)((blockIdx.x / p.splits * 5u + blockIdx.y * 3u) % (unsigned)kr.n);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kG4WStages; ++s) {
@@ -124,7 +238,7 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
       mbar_init(&xfull[s], 1);
       mbar_init(&xempty[s], 1);
     }
-    for (int s = 0; s < kG4Slots; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(&afull[s], 4);
       mbar_init(&aempty[s], 1);
     }
@@ -135,8 +249,8 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
     tc::prefetch_tmap(&tmW);
     tc::prefetch_tmap(&tmX);
   }
-  if (warp == kG4MmaWarp) {
-    tc::tmem_alloc(tmem_holder, Cfg::kTmem);
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tmem_holder, 256);
     tc::tmem_relinquish();
   }
   __syncthreads();
@@ -151,7 +265,7 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
     const G4Tile tile = live ? p.tiles[blockIdx.y] : G4Tile{0, 0, 0, 0};
     e = tile.expert;
     count = tile.count;
-    for (int i = threadIdx.x; i < p.ntok && count > 0; i += kG4Threads) {
+    for (int i = threadIdx.x; i < p.ntok && count > 0; i += kThreads) {
       const int pair = p.order[tile.start + min(i, count - 1)];
       const int row = pair / p.rows_per_token;
       const int ex = p.ex[row];
@@ -164,7 +278,7 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
   } else {
     m0 = (int64_t)blockIdx.y * p.ntok;
     count = (int)min((int64_t)p.ntok, p.M - m0);
-    for (int i = threadIdx.x; i < count; i += kG4Threads) {
+    for (int i = threadIdx.x; i < count; i += kThreads) {
       const int ex = p.ex[m0 + i];
       s_ex[i] = ex;
       s_fac[i] = exp2i(max(-126, min(126, -ex)));
@@ -175,174 +289,115 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tmem_holder;
-  const uint32_t tmem_a = tmem + RT * Cfg::kDCols;
+  const uint32_t tmem_a = tmem + 128;
   const int mma_n = (count + 15) & ~15;
 
-  if (count > 0 && warp == kG4TmaWarp) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const uint64_t pol_w = l2_policy_evict_first();
-      const uint64_t pol_x = l2_policy_evict_last();
-      const int wrow = (int)(e * p.N + n0);
-      const uint32_t xbytes = kExperts ? (uint32_t)((count + 3) / 4) * 512u : (uint32_t)p.ntok * 128u;
-      bool ok = true;
-      int jw = 0, jx = 0;  // issued stages
-      int s = 0;           // token stage of granule j, and how often it was filled
-      uint32_t fill = 0;
-      for (int j = 0; j < ngran && ok; ++j) {
-        if (j % 4 == 0) {
-          const int v = jw % kG4WStages;
-          if (jw >= kG4WStages) ok = mbar_wait_bounded(&wempty[v], ((jw / kG4WStages) - 1) & 1, abort_flag);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&wfull[v], Cfg::kWBytes);
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-            tc::tma_load_2d(wring + v * Cfg::kWBytes + r * 16384, &tmW, (w0 + jw) * 128, wrow + r * 128, &wfull[v],
-                            pol_w);
-          ++jw;
-        }
-        if (fill > 0) ok = mbar_wait_bounded(&xempty[s], (fill - 1) & 1, abort_flag);
+  if (count > 0 && warp >= kG4DequantWarps && warp < kMmaWarp) {
+    // ------------------------------------------------------------ TMA producers
+    const int pw = warp - kG4DequantWarps;
+    const uint64_t pol_w = l2_policy_evict_first();
+    const uint64_t pol_x = l2_policy_evict_last();
+    const int wrow = (int)(e * p.N + n0);
+    const uint32_t xbytes = kExperts ? (uint32_t)((count + 3) / 4) * 512u : (uint32_t)p.ntok * 128u;
+    bool ok = true;
+    int jw = 0, jx = 0;  // issued stages
+    int s = 0;           // token stage of the next granule, and how often it was filled
+    uint32_t fill = 0;
+    for (; jw < kr.n && ok; ++jw) {
+      const int v = jw % kG4WStages, w = kr.stage(jw);
+      if (pw == 0) {
+        if (jw >= kG4WStages) ok = w4::wait(&wempty[v], ((jw / kG4WStages) - 1) & 1, abort_flag);
         if (!ok) break;
-        mbar_arrive_expect_tx(&xfull[s], xbytes);
-        uint8_t* dst = xring + s * p.xstage;
-        const int xb = (w0 * 4 + j) * 128;
-        if constexpr (kExperts) {
-          for (int i = 0; i < count; i += 4)
-            w4::tma_gather4(dst + i * 128, &tmX, xb, *reinterpret_cast<const int4*>(s_row + i), &xfull[s]);
-        } else {
-          tc::tma_load_2d(dst, &tmX, xb, (int)m0, &xfull[s], pol_x);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&wfull[v], kNarrowWBytes);
+          tc::tma_load_2d(wring + v * kNarrowWBytes, &tmW, w * 128, wrow, &wfull[v], pol_w);
         }
+        __syncwarp();
+      }
+      const int ng = kr.granules(w);
+      for (int gq = 0; gq < ng; ++gq) {
+        if (fill > 0) ok = w4::wait(&xempty[s], (fill - 1) & 1, abort_flag);
+        if (!ok) break;
+        load_tokens<kExperts>(tmX, xring + s * p.xstage, &xfull[s], xbytes, (w * 4 + gq) * 128, (int)m0, s_row,
+                              count, pw, lane, pol_x);
         ++jx;
         if (++s == xs_n) {
           s = 0;
           ++fill;
         }
       }
-      if (!ok) {
-        if (!*abort_flag) record_timeout(p.status, KID_W4, 1);
-        *abort_flag = 1;
-        // the copies in flight land before the CTA leaves
-        for (int j = max(0, jw - kG4WStages); j < jw; ++j)
-          mbar_wait_bounded(&wfull[j % kG4WStages], (j / kG4WStages) & 1, nullptr);
-        for (int j = max(0, jx - xs_n); j < jx; ++j) mbar_wait_bounded(&xfull[j % xs_n], (j / xs_n) & 1, nullptr);
-      }
     }
-  } else if (count > 0 && warp == kG4MmaWarp) {
+    if (!ok) {
+      if (lane == 0 && !*abort_flag) record_timeout(p.status, KID_W4, 1);
+      *abort_flag = 1;
+      // the copies in flight land before the CTA leaves
+      for (int j = max(0, jw - kG4WStages); j < jw && pw == 0; ++j)
+        mbar_wait_bounded(&wfull[j % kG4WStages], (j / kG4WStages) & 1, nullptr);
+      for (int j = max(0, jx - xs_n); j < jx; ++j) mbar_wait_bounded(&xfull[j % xs_n], (j / xs_n) & 1, nullptr);
+    }
+  } else if (count > 0 && warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t id = w4::idesc_f16(128, mma_n);
-      bool ok = true;
-      int xs = 0;
-      uint32_t xphase = 0;
-      for (int j = 0; j < ngran && ok; ++j) {
-        ok = mbar_wait_bounded(&xfull[xs], xphase, abort_flag);
-        const uint64_t bdesc = tc::sw128_desc(smem_u32(xring + xs * p.xstage));
+    const uint32_t id = w4::idesc_f16(128, mma_n);
+    const uint32_t elected = w4::elect_one();
+    const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0), a = d + 128;  // warp-uniform
+    const uint32_t x0 = smem_u32(xring);
+    const int ngran = kr.total();
+    bool ok = true;
+    int xs = 0;
+    uint32_t xphase = 0;
+    for (int j = 0; j < ngran; ++j) {
+      const int slot = j % kSlots;
+      ok = w4::wait(&xfull[xs], xphase, abort_flag);
+      ok = ok && w4::wait(&afull[slot], (j / kSlots) & 1, abort_flag);
+      if (!ok) break;
+      tc::fence_after();
+      const uint64_t bdesc = tc::sw128_desc(x0 + xs * p.xstage);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const int use = RT == 2 ? j / 2 : j / 4;              // how often the slot was used before
-          const int slot = RT == 2 ? r * 2 + (j & 1) : j & 3;
-          ok = ok && mbar_wait_bounded(&afull[slot], use & 1, abort_flag);
-          if (!ok) break;
-          tc::fence_after();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w4::mma_f16_ts(tmem + r * Cfg::kDCols, tmem_a + slot * 32 + k * 8, bdesc + 2 * k, id, j > 0 || k > 0);
-          tc::commit(&aempty[slot]);
-        }
-        if (ok) tc::commit(&xempty[xs]);
-        if (++xs == xs_n) {
-          xs = 0;
-          xphase ^= 1;
-        }
+      for (int k = 0; k < 4; ++k)
+        w4::mma_f16_ts(d, a + slot * 32 + k * 8, bdesc + 2 * k, id, j > 0 || k > 0, elected);
+      w4::commit(&aempty[slot], elected);
+      w4::commit(&xempty[xs], elected);
+      if (++xs == xs_n) {
+        xs = 0;
+        xphase ^= 1;
       }
-      if (!ok) {
-        if (!*abort_flag) record_timeout(p.status, KID_W4, 2);
-        *abort_flag = 1;
-      }
-      tc::commit(done);
-      mbar_wait_bounded(done, 0, nullptr);
     }
+    if (!ok) {
+      if (lane == 0 && !*abort_flag) record_timeout(p.status, KID_W4, 2);
+      *abort_flag = 1;
+    }
+    w4::commit(done, elected);
+    w4::wait(done, 0, nullptr);
   } else if (count > 0 && warp < kG4DequantWarps) {
     // ------------------------------------------------------------ codes -> TMEM
-    // RT = 2: each four warps take a row tile; RT = 1: they take alternate granules.
+    // Warps 0-3 take the even granules, 4-7 the odd ones; thread = weight row.
     const int wg = warp >> 2, q = warp & 3;
-    const int r = RT == 2 ? wg : 0;
-    const int64_t n = n0 + r * 128 + q * 32 + lane;
+    const int64_t n = n0 + q * 32 + lane;
     const int64_t wr = e * p.N + min(n, p.N - 1);
     const uint16_t* sw = p.sw + wr * p.groups;
     const uint8_t* wz = kZero ? p.wz + wr * p.groups : nullptr;
-    const int g0 = w0 * kPerStage, g1 = min(p.groups, w1 * kPerStage);
-    // the row's exponent: its largest |s| to [2^10, 2^11)
-    uint32_t top = 0;
-    if ((p.groups & 7) == 0) {
-      const uint4* v4 = reinterpret_cast<const uint4*>(sw);
-#pragma unroll 4
-      for (int i = g0 >> 3; i < (g1 + 7) >> 3; ++i) {
-        const uint4 v = __ldg(v4 + i);
-        top = max(max(max(top, v.x & 0x7FFFu), max(v.x >> 16 & 0x7FFFu, v.y & 0x7FFFu)),
-                  max(max(v.y >> 16 & 0x7FFFu, v.z & 0x7FFFu),
-                      max(v.z >> 16 & 0x7FFFu, max(v.w & 0x7FFFu, v.w >> 16 & 0x7FFFu))));
-      }
-    } else {
-#pragma unroll 8
-      for (int i = g0; i < g1; ++i) top = max(top, (uint32_t)__ldg(sw + i) & 0x7FFFu);
-    }
-    top = min(top, 0x7F7Fu);
-    // exponent of a bf16: the biased field, or for a subnormal the place of its top bit
-    const int p2 = top >= 0x80u ? (int)(top >> 7) - 127 : top ? -133 + (31 - __clz(top)) : 10;
-    const int f = 10 - p2;
+    G4Scales<kGroup, kZero> sc;
+    const int f = row_exponent(sw, kr.w0 * sc.kN, min(p.groups, (kr.w0 + kr.n) * sc.kN), (p.groups & 7) == 0);
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
-    const uint32_t rsw = (uint32_t)(lane & 7);
-    const uint32_t row_off = (uint32_t)(r * 16384 + (q * 32 + lane) * 128);
-
-    uint32_t sraw[kPerStage], zraw[kPerStage];
-    auto load_scales = [&](int w) {
-#pragma unroll
-      for (int i = 0; i < kPerStage; ++i) {
-        const int gi = w * kPerStage + i;
-        sraw[i] = gi < p.groups ? __ldg(sw + gi) : 0;
-        if constexpr (kZero) zraw[i] = gi < p.groups ? __ldg(wz + gi) : 8;
-      }
-    };
-    load_scales(w0);
+    const uint32_t row_off = (uint32_t)((q * 32 + lane) * 128);
+    sc.load(sw, wz, kr.stage(0), p.groups);
     bool ok = true;
-    for (int w = w0; w < w1 && ok; ++w) {
-      const int jw = w - w0, ws = jw % kG4WStages;
-      uint32_t s2[kPerStage], zlo[kPerStage], zhi[kPerStage];
-#pragma unroll
-      for (int i = 0; i < kPerStage; ++i) {
-        const float s = scale2(__uint_as_float(sraw[i] << 16), f);
-        s2[i] = w4::f32x2_to_f16x2(s, s);
-        if constexpr (kZero) {
-          zlo[i] = 0x64006400u + zraw[i] * 0x10001u;
-          const float zf = -(64.0f + (float)zraw[i]);
-          zhi[i] = w4::f32x2_to_f16x2(zf, zf);
-        } else {
-          zlo[i] = 0x64086408u;  // 1032
-          zhi[i] = 0xD480D480u;  // -72
-        }
-      }
-      if (w + 1 < w1) load_scales(w + 1);
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&wfull[ws], (jw / kG4WStages) & 1, abort_flag));
+    int j = 0;  // granule
+    for (int jw = 0; jw < kr.n && ok; ++jw) {
+      const int ws = jw % kG4WStages, ng = kr.granules(kr.stage(jw));
+      sc.convert(f);
+      if (jw + 1 < kr.n) sc.load(sw, wz, kr.stage(jw + 1), p.groups);
+      ok = w4::wait(&wfull[ws], (jw / kG4WStages) & 1, abort_flag);
       if (!ok) break;
-      const uint8_t* src = wring + ws * Cfg::kWBytes + row_off;
+      const uint8_t* src = wring + ws * kNarrowWBytes + row_off;
 #pragma unroll
-      for (int gq = 0; gq < 4; ++gq) {
-        const int j = jw * 4 + gq;
-        if (j >= ngran) break;
-        if (RT == 1 && (gq & 1) != wg) continue;
-        const uint4 c0 = *reinterpret_cast<const uint4*>(src + (((uint32_t)(2 * gq) ^ rsw) << 4));
-        const uint4 c1 = *reinterpret_cast<const uint4*>(src + (((uint32_t)(2 * gq + 1) ^ rsw) << 4));
-        const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+      for (int gq = 0; gq < 4; ++gq, ++j) {
+        if (gq >= ng) break;
+        if ((j & 1) != wg) continue;
         uint32_t h[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int gi = (gq * 64 + i * 8) / kGroup;
-          w4::codes_to_f16(c[i], zlo[gi], zhi[gi], s2[gi], h + 4 * i);
-        }
-        const int use = RT == 2 ? j / 2 : j / 4;
-        const int slot = RT == 2 ? r * 2 + (j & 1) : j & 3;
-        if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&aempty[slot], (use - 1) & 1, abort_flag));
+        sc.granule(src, gq, (uint32_t)(lane & 7), h);
+        const int slot = j % kSlots, use = j / kSlots;
+        if (use > 0) ok = w4::wait(&aempty[slot], (use - 1) & 1, abort_flag);
         if (!ok) break;
         tc::fence_after();
         w4::st32(tmem_a + slot * 32 + lane_addr, h);
@@ -360,48 +415,38 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
       *abort_flag = 1;
     }
     // ------------------------------------------------------------ epilogue
-    ok = ok && mbar_wait_bounded(done, 0, abort_flag) && !*abort_flag;
-    ok = __all_sync(0xffffffffu, ok);
+    ok = ok && w4::wait(done, 0, abort_flag);
+    ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     if (ok) {
       tc::fence_after();
-      // Staged in the rings, which every MMA has left behind: split K, [tok][128 RT]
-      // partial sums; else [tok][128 RT] bf16 (rows padded by 16 bytes), so that the
-      // rows leave in 16-byte stores, 512 or 256 bytes of a token together.
-      constexpr int kRow = RT * 128 * 2 + 16;
+      // Staged in the rings, which every MMA has left behind: split K, [tok][128]
+      // partial sums; else [tok][128] bf16 (rows padded by 16 bytes), so that the rows
+      // leave in 16-byte stores.
+      constexpr int kRow = 128 * 2 + 16;
       float* part = reinterpret_cast<float*>(wring);
-      const int col = r * 128 + q * 32 + lane;
+      const int col = q * 32 + lane;
       const int half = ((mma_n / 16 + 1) / 2) * 16;
-      const int c_lo = RT == 2 ? 0 : wg ? half : 0, c_hi = RT == 2 ? mma_n : wg ? mma_n : half;
+      const int c_lo = wg ? half : 0, c_hi = wg ? mma_n : half;
       const bool wide = __any_sync(0xffffffffu, *s_wide || abs(f) > 60);
       const float rf = exp2i(max(-126, min(126, -f)));
       for (int c = c_lo; c < c_hi; c += 16) {
-        uint32_t v[16];
-        w4::ld16(tmem + r * Cfg::kDCols + lane_addr + c, v);
-        tc::ld_wait();
         float o[16];
+        uint32_t v[16];
+        w4::ld16(tmem + lane_addr + c, v);
+        tc::ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(v[i]) * rf * s_fac[c + i];
-        if (wide) {  // the two factors together may leave f32's range where their product does not
-#pragma unroll 1
-          for (int i = 0; i < 16; ++i)
-            if (c + i < count) {
-              uint32_t one[1];
-              w4::ld1(tmem + r * Cfg::kDCols + lane_addr + c + i, one);
-              tc::ld_wait();
-              const float t = scale2(__uint_as_float(one[0]), -(f + s_ex[c + i]));
-              if (p.splits > 1)
-                part[(c + i) * (RT * 128) + col] = t;
-              else
-                *reinterpret_cast<uint16_t*>(wring + (c + i) * kRow + col * 2) = f32_to_bf16_rn(t);
-            }
-        } else if (p.splits > 1) {
+        for (int i = 0; i < 16; ++i) {
+          const float acc = __uint_as_float(v[i]);
+          // wide: the two factors may leave f32's range where their product does not
+          o[i] = !wide ? acc * rf * s_fac[c + i] : c + i < count ? scale2(acc, -(f + s_ex[c + i])) : 0.0f;
+        }
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i < count) part[(c + i) * (RT * 128) + col] = o[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i < count) *reinterpret_cast<uint16_t*>(wring + (c + i) * kRow + col * 2) = f32_to_bf16_rn(o[i]);
+        for (int i = 0; i < 16; ++i) {
+          if (c + i >= count) continue;
+          if (p.splits > 1)
+            part[(c + i) * 128 + col] = o[i];
+          else
+            *reinterpret_cast<uint16_t*>(wring + (c + i) * kRow + col * 2) = f32_to_bf16_rn(o[i]);
         }
       }
       tc::fence_before();
@@ -412,18 +457,17 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
   if (p.splits > 1) {
     // the cluster's partial sums, added in the order of their K ranges
     w4::cluster_sync();
-    if (warp == kG4MmaWarp) {
+    if (warp == kMmaWarp) {
       tc::fence_after();
-      tc::tmem_dealloc(tmem, Cfg::kTmem);
+      tc::tmem_dealloc(tmem, 256);
     }
     if (!*abort_flag) {
       const uint32_t part = smem_u32(wring);
-      for (int i = threadIdx.x; i < RT * 128 * ((count - split + p.splits - 1) / p.splits); i += kG4Threads) {
-        const int c = (i / (RT * 128)) * p.splits + split, col = i % (RT * 128);
+      for (int i = threadIdx.x; i < 128 * ((count - split + p.splits - 1) / p.splits); i += kThreads) {
+        const int c = (i / 128) * p.splits + split, col = i % 128;
         if (n0 + col >= p.N) continue;
         float sum = 0.0f;
-        for (int s = 0; s < p.splits; ++s)
-          sum += w4::ld_cluster(part + (uint32_t)(c * (RT * 128) + col) * 4u, (uint32_t)s);
+        for (int s = 0; s < p.splits; ++s) sum += w4::ld_cluster(part + (uint32_t)(c * 128 + col) * 4u, (uint32_t)s);
         p.y[(m0 + c) * p.N + n0 + col] = f32_to_bf16_rn(sum);
       }
     }
@@ -433,30 +477,373 @@ __global__ void __launch_bounds__(kG4Threads, RT == 2 ? 1 : 2)
     __syncthreads();
     // before the copies below, in which a warp's lanes may part: dealloc is a
     // whole-warp instruction
-    if (warp == kG4MmaWarp) {
+    if (warp == kMmaWarp) {
       tc::fence_after();
-      tc::tmem_dealloc(tmem, Cfg::kTmem);
+      tc::tmem_dealloc(tmem, 256);
     }
     if (count > 0 && !*abort_flag) {
-      constexpr int kRow = RT * 128 * 2 + 16;
-      constexpr int kVecs = RT * 16;  // 16-byte pieces of a token's row
-      const int cols = (int)min((int64_t)(RT * 128), p.N - n0);
+      constexpr int kRow = 128 * 2 + 16;
+      const int cols = (int)min((int64_t)128, p.N - n0);
       if ((p.N & 7) == 0) {
-        for (int i = threadIdx.x; i < count * kVecs; i += kG4Threads) {
-          const int c = i / kVecs, b = i % kVecs;
+        for (int i = threadIdx.x; i < count * 16; i += kThreads) {
+          const int c = i / 16, b = i % 16;
           const int64_t row = kExperts ? s_out[c] : m0 + c;
           if (b * 8 < cols)
             *reinterpret_cast<uint4*>(p.y + row * p.N + n0 + b * 8) =
                 *reinterpret_cast<const uint4*>(wring + c * kRow + b * 16);
         }
       } else {
-        for (int i = threadIdx.x; i < count * RT * 128; i += kG4Threads) {
-          const int c = i / (RT * 128), b = i % (RT * 128);
+        for (int i = threadIdx.x; i < count * 128; i += kThreads) {
+          const int c = i / 128, b = i % 128;
           const int64_t row = kExperts ? s_out[c] : m0 + c;
           if (b < cols) p.y[row * p.N + n0 + b] = *reinterpret_cast<const uint16_t*>(wring + c * kRow + b * 2);
         }
       }
     }
+  }
+}
+
+// ---------------------------------------------------------------------------- wide
+
+// One tile of the persistent kernel: a row tile of 256 weights and up to ntok tokens.
+struct WideTile {
+  int64_t e, m0;
+  int start, count, rt, tt;
+};
+
+template <bool kExperts>
+QL_DEVINL WideTile wide_tile(const G4Params& p, int t) {
+  WideTile w;
+  w.tt = t / p.row_tiles;
+  w.rt = t - w.tt * p.row_tiles;
+  if constexpr (kExperts) {
+    const G4Tile g = p.tiles[w.tt];
+    w.e = g.expert;
+    w.start = g.start;
+    w.count = g.count;
+    w.m0 = 0;
+  } else {
+    w.e = 0;
+    w.start = 0;
+    w.m0 = (int64_t)w.tt * p.ntok;
+    w.count = (int)min((int64_t)p.ntok, p.M - w.m0);
+  }
+  return w;
+}
+
+// Any of the epilogue's threads (a barrier among them).
+QL_DEVINL bool wide_epi_any(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "n"(kWideEpiWarps * 32)
+      : "memory");
+  return r != 0;
+}
+
+template <int kGroup, bool kZero, bool kExperts>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    w4_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const G4Params p) {
+  const int xs_n = p.xstages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* wring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* xring = wring + kG4WStages * kWideWBytes;
+  uint8_t* staging = xring + xs_n * p.xstage;
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(staging + kWideEpiWarps * 16 * kWideStageRow);
+  uint64_t* wempty = wfull + kG4WStages;
+  uint64_t* xfull = wempty + kG4WStages;
+  uint64_t* xempty = xfull + kG4MaxXStages;
+  uint64_t* afull = xempty + kG4MaxXStages;
+  uint64_t* aempty = afull + 2;
+  uint64_t* dfull = aempty + 2;
+  uint64_t* dempty = dfull + 1;
+  // [4][256] the rows' exponents: with short K the dequantizing warps are up to three
+  // tiles ahead of the epilogue
+  int* s_f = reinterpret_cast<int*>(wfull + 32);
+  int* s_row = s_f + 4 * 256;                                     // [2][kWideTok] experts: x rows
+  int* s_out = s_row + 2 * kWideTok;                              // [2][kWideTok] experts: pairs
+  int* s_ex = s_out + 2 * kWideTok;                               // [2][kWideTok] the columns' exponents
+  float* s_fac = reinterpret_cast<float*>(s_ex + 2 * kWideTok);   // [2][kWideTok] 2^-exponent
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_fac + 2 * kWideTok);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  G4Range kr;
+  kr.nk64 = (int)((p.K + kG4GranK - 1) / kG4GranK);
+  kr.w0 = 0;
+  kr.n = (int)((p.K + kG4StageK - 1) / kG4StageK);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kG4WStages; ++s) {
+      mbar_init(&wfull[s], 1);
+      mbar_init(&wempty[s], kG4DequantWarps);
+    }
+    for (int s = 0; s < xs_n; ++s) {
+      mbar_init(&xfull[s], 1);
+      mbar_init(&xempty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&afull[s], kG4DequantWarps);
+      mbar_init(&aempty[s], 1);
+    }
+    mbar_init(dfull, 1);
+    mbar_init(dempty, kWideEpiWarps);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tc::prefetch_tmap(&tmW);
+    tc::prefetch_tmap(&tmX);
+  }
+  if (warp == kWideMma) {
+    tc::tmem_alloc(tmem_holder, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmem_a = tmem + 2 * kWideTok;
+  tc::grid_dependency_wait();  // the prepare kernel's tokens, pairs and tiles
+  tc::launch_dependents();
+  const int tiles = p.row_tiles * (kExperts ? *p.ntiles : p.tok_tiles);
+  bool ok = true;
+
+  if (warp >= kWideFirstProducer && warp < kWideMma) {
+    // ------------------------------------------------------------ TMA producers
+    const int pw = warp - kWideFirstProducer;
+    const uint64_t pol_w = l2_policy_evict_first();
+    const uint64_t pol_x = l2_policy_evict_last();
+    int jw = 0, jx = 0;  // issued stages
+    int s = 0;           // token stage of the next granule, and how often it was filled
+    uint32_t fill = 0;
+    int it = 0;
+    for (int t = blockIdx.x; t < tiles && ok && (kExperts || pw == 0); t += gridDim.x, ++it) {
+      const WideTile w = wide_tile<kExperts>(p, t);
+      kr.rot = (w.rt * 5 + w.tt * 3) % kr.n;
+      const int* rows = s_row + (it & 1) * kWideTok;
+      if constexpr (kExperts) {
+        for (int i = threadIdx.x - kWideFirstProducer * 32; i < ((w.count + 3) & ~3); i += kG4Producers * 32)
+          s_row[(it & 1) * kWideTok + i] = p.order[w.start + min(i, w.count - 1)] / p.rows_per_token;
+        named_bar_sync(2, kG4Producers * 32);
+      }
+      const int wrow = (int)(w.e * p.N + (int64_t)w.rt * 256);
+      const uint32_t xbytes = kExperts ? (uint32_t)((w.count + 3) / 4) * 512u : (uint32_t)p.ntok * 128u;
+      for (int j = 0; j < kr.n && ok; ++j, ++jw) {
+        const int v = jw % kG4WStages, ws = kr.stage(j);
+        if (pw == 0) {
+          if (jw >= kG4WStages) ok = w4::wait(&wempty[v], ((jw / kG4WStages) - 1) & 1, abort_flag);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&wfull[v], kWideWBytes);
+            tc::tma_load_2d(wring + v * kWideWBytes, &tmW, ws * 128, wrow, &wfull[v], pol_w);
+            tc::tma_load_2d(wring + v * kWideWBytes + 16384, &tmW, ws * 128, wrow + 128, &wfull[v], pol_w);
+          }
+          __syncwarp();
+        }
+        const int ng = kr.granules(ws);
+        for (int gq = 0; gq < ng; ++gq) {
+          if (fill > 0) ok = w4::wait(&xempty[s], (fill - 1) & 1, abort_flag);
+          if (!ok) break;
+          load_tokens<kExperts>(tmX, xring + s * p.xstage, &xfull[s], xbytes, (ws * 4 + gq) * 128, (int)w.m0, rows,
+                                w.count, pw, lane, pol_x);
+          ++jx;
+          if (++s == xs_n) {
+            s = 0;
+            ++fill;
+          }
+        }
+      }
+    }
+    if (!ok) {
+      if (lane == 0 && !*abort_flag) record_timeout(p.status, KID_W4, 4);
+      *abort_flag = 1;
+      // the copies in flight land before the CTA leaves
+      for (int j = max(0, jw - kG4WStages); j < jw && pw == 0; ++j)
+        mbar_wait_bounded(&wfull[j % kG4WStages], (j / kG4WStages) & 1, nullptr);
+      for (int j = max(0, jx - xs_n); j < jx; ++j) mbar_wait_bounded(&xfull[j % xs_n], (j / xs_n) & 1, nullptr);
+    }
+  } else if (warp == kWideMma) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t elected = w4::elect_one();
+    const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0), a = d + 2 * kWideTok;  // warp-uniform
+    const uint32_t x0 = smem_u32(xring);
+    const int ngran = kr.total();
+    int xs = 0, g = 0, it = 0;  // g: granules over all tiles
+    uint32_t xphase = 0;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++it) {
+      const WideTile w = wide_tile<kExperts>(p, t);
+      const uint32_t id = w4::idesc_f16(128, (w.count + 15) & ~15);
+      if (it > 0) ok = w4::wait(dempty, (it - 1) & 1, abort_flag);  // the last tile's sums are read
+      for (int j = 0; j < ngran && ok; ++j, ++g) {
+        const int slot = g & 1;
+        ok = w4::wait(&xfull[xs], xphase, abort_flag);
+        ok = ok && w4::wait(&afull[slot], (g >> 1) & 1, abort_flag);
+        if (!ok) break;
+        tc::fence_after();
+        const uint64_t bdesc = tc::sw128_desc(x0 + xs * p.xstage);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w4::mma_f16_ts(d + r * kWideTok, a + (r * 2 + slot) * 32 + k * 8, bdesc + 2 * k, id, j > 0 || k > 0,
+                           elected);
+        w4::commit(&aempty[slot], elected);
+        w4::commit(&xempty[xs], elected);
+        if (++xs == xs_n) {
+          xs = 0;
+          xphase ^= 1;
+        }
+      }
+      if (!ok) break;
+      w4::commit(dfull, elected);
+    }
+    if (!ok) {
+      if (lane == 0 && !*abort_flag) record_timeout(p.status, KID_W4, 5);
+      *abort_flag = 1;
+      // the products in flight end before the CTA leaves
+      w4::commit(dfull, elected);
+      w4::wait(dfull, it & 1, nullptr);
+    }
+  } else if (warp < kG4DequantWarps) {
+    // ------------------------------------------------------------ codes -> TMEM
+    // Each four warps take a row tile; thread = weight row.
+    const int r = warp >> 2, q = warp & 3;
+    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    const uint32_t row = (uint32_t)(r * 128 + q * 32 + lane);
+    int g = 0, jw = 0, it = 0;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++it) {
+      const WideTile w = wide_tile<kExperts>(p, t);
+      kr.rot = (w.rt * 5 + w.tt * 3) % kr.n;
+      const int64_t wr = w.e * p.N + min((int64_t)w.rt * 256 + row, p.N - 1);
+      const uint16_t* sw = p.sw + wr * p.groups;
+      const uint8_t* wz = kZero ? p.wz + wr * p.groups : nullptr;
+      G4Scales<kGroup, kZero> sc;
+      sc.load(sw, wz, kr.stage(0), p.groups);
+      const int f = row_exponent(sw, 0, p.groups, (p.groups & 7) == 0);
+      s_f[(it & 3) * 256 + row] = f;
+      for (int j = 0; j < kr.n && ok; ++j, ++jw) {
+        const int ws = jw % kG4WStages, ng = kr.granules(kr.stage(j));
+        sc.convert(f);
+        if (j + 1 < kr.n) sc.load(sw, wz, kr.stage(j + 1), p.groups);
+        ok = w4::wait(&wfull[ws], (jw / kG4WStages) & 1, abort_flag);
+        if (!ok) break;
+        const uint8_t* src = wring + ws * kWideWBytes + row * 128;
+#pragma unroll
+        for (int gq = 0; gq < 4; ++gq) {
+          if (gq >= ng) break;
+          uint32_t h[32];
+          sc.granule(src, gq, (uint32_t)(lane & 7), h);
+          const int slot = g & 1, use = g >> 1;
+          if (use > 0) ok = w4::wait(&aempty[slot], (use - 1) & 1, abort_flag);
+          if (!ok) break;
+          tc::fence_after();
+          w4::st32(tmem_a + (r * 2 + slot) * 32 + lane_addr, h);
+          w4::st_wait();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&afull[slot]);
+          ++g;
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&wempty[ws]);
+      }
+    }
+    if (!ok) {
+      if (lane == 0 && !*abort_flag) record_timeout(p.status, KID_W4, 6);
+      *abort_flag = 1;
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    // While the next tile's first weights are dequantized: a warp's 32 rows, 16 tokens
+    // at a time, through its own staging so that they leave in 16-byte stores.
+    const int ew = warp - kWideFirstEpi, r = ew >> 2, q = warp & 3;
+    const int et = threadIdx.x - kWideFirstEpi * 32;
+    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    uint8_t* stg = staging + ew * 16 * kWideStageRow;
+    const bool vec = (p.N & 7) == 0;
+    int it = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+      const WideTile w = wide_tile<kExperts>(p, t);
+      const int buf = (it & 1) * kWideTok;
+      bool wide = false;
+      if (et < w.count) {
+        int64_t xrow = w.m0 + et;
+        if constexpr (kExperts) {
+          const int pair = p.order[w.start + et];
+          s_out[buf + et] = pair;
+          xrow = pair / p.rows_per_token;
+        }
+        const int ex = p.ex[xrow];
+        s_ex[buf + et] = ex;
+        s_fac[buf + et] = exp2i(max(-126, min(126, -ex)));
+        wide = abs(ex) > 60;
+      }
+      wide = wide_epi_any(wide);  // an exponent that one factor cannot take
+      ok = w4::wait(dfull, it & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+      if (wide_epi_any(!ok)) break;
+      tc::fence_after();
+      const int f = s_f[(it & 3) * 256 + r * 128 + q * 32 + lane];
+      wide = __any_sync(0xffffffffu, wide || abs(f) > 60);
+      const float rf = exp2i(max(-126, min(126, -f)));
+      const int64_t nw = (int64_t)w.rt * 256 + r * 128 + q * 32;  // the warp's first output
+      const int mma_n = (w.count + 15) & ~15;
+      for (int c = 0; c < mma_n; c += 16) {
+        uint32_t v[16];
+        w4::ld16(tmem + r * kWideTok + lane_addr + c, v);
+        tc::ld_wait();
+        if (c + 16 >= mma_n) {
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(dempty);
+        }
+        float o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float acc = __uint_as_float(v[i]);
+          // wide: the two factors may leave f32's range where their product does not
+          o[i] = !wide ? acc * rf * s_fac[buf + c + i]
+                       : c + i < w.count ? scale2(acc, -(f + s_ex[buf + c + i])) : 0.0f;
+        }
+        if (vec) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<uint16_t*>(stg + i * kWideStageRow + lane * 2) = f32_to_bf16_rn(o[i]);
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int tok = h * 8 + (lane >> 2), piece = lane & 3;
+            const int64_t n = nw + piece * 8;
+            if (c + tok < w.count && n < p.N) {
+              const int64_t orow = kExperts ? s_out[buf + c + tok] : w.m0 + c + tok;
+              *reinterpret_cast<uint4*>(p.y + orow * p.N + n) =
+                  *reinterpret_cast<const uint4*>(stg + tok * kWideStageRow + piece * 16);
+            }
+          }
+          __syncwarp();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c + i >= w.count || nw + lane >= p.N) continue;
+            const int64_t orow = kExperts ? s_out[buf + c + i] : w.m0 + c + i;
+            p.y[orow * p.N + nw + lane] = f32_to_bf16_rn(o[i]);
+          }
+        }
+      }
+    }
+    if (!ok) {
+      if (lane == 0 && !*abort_flag) record_timeout(p.status, KID_W4, 7);
+      *abort_flag = 1;
+    }
+  }
+
+  __syncwarp();
+  __syncthreads();
+  if (warp == kWideMma) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem, 512);
   }
 }
 
@@ -527,8 +914,8 @@ QL_DEVINL void plan_experts(const G4PrepParams& p, int* hist) {
     ti += warp_sums[1][warp - 1];
   }
   base[tid] = ci - c;
-  for (int i = 0; i < t; ++i)
-    p.tiles[ti - t + i] = G4Tile{tid, ci - c + i * p.ntok, min(p.ntok, c - i * p.ntok), 0};
+  const int per = t ? ((c + t - 1) / t + 15) & ~15 : 0;  // an expert's tiles are alike
+  for (int i = 0; i < t; ++i) p.tiles[ti - t + i] = G4Tile{tid, ci - c + i * per, min(per, c - i * per), 0};
   if (tid == kG4PlanThreads - 1) *p.ntiles = ti;
   __syncthreads();
   for (int64_t i = tid; i < p.pairs; i += kG4PlanThreads) {
@@ -559,8 +946,7 @@ QL_DEVINL void prepare_row(const G4PrepParams& p, int64_t row, int tid, int thre
   __syncthreads();
   top = 0;
   for (int i = 0; i < threads / 32; ++i) top = max(top, r[i]);
-  const int p2 = top >= 0x80u ? (int)(top >> 7) - 127 : top ? -133 + (31 - __clz(top)) : 14;
-  const int e = 14 - p2;
+  const int e = 14 - log2_bf16(top, 14);
   if (tid == 0) p.ex[row] = e;
   const float f0 = exp2i(e / 2), f1 = exp2i(e - e / 2);
   for (int i = tid; i < chunks; i += threads) {
@@ -630,7 +1016,8 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restr
 namespace {
 
 struct G4Plan {
-  int rt, ntok, splits;
+  bool wide;
+  int ntok, splits;
   unsigned row_tiles, tok_tiles;
 };
 
@@ -639,22 +1026,22 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 G4Plan plan_dense(int64_t M, const ql_w4_weight& w, int sms) {
   G4Plan g;
   if (M > 128) {
-    g.rt = 2;
+    g.wide = true;
     g.row_tiles = (unsigned)div_up(w.N, 256);
-    g.ntok = 192;
+    g.splits = 1;
+    // tokens of a tile: fewest rounds of the SMs, each round's time about its tokens
+    g.ntok = kWideTok;
     double best = 1e30;
-    for (int n = 192; n >= 96; n -= 16) {
-      const int64_t tt = div_up(M, n);
-      const double cost = (double)div_up(g.row_tiles * tt, sms) * (n + 16);
+    for (int n = kWideTok; n >= 96; n -= 16) {
+      const double cost = (double)div_up(g.row_tiles * div_up(M, n), sms) * (n + 16);
       if (cost < best) {
         best = cost;
         g.ntok = n;
       }
     }
     g.tok_tiles = (unsigned)div_up(M, g.ntok);
-    g.splits = 1;
   } else {
-    g.rt = 1;
+    g.wide = false;
     g.row_tiles = (unsigned)div_up(w.N, 128);
     g.ntok = (int)div_up(M, 16) * 16;
     g.tok_tiles = 1;
@@ -670,15 +1057,9 @@ G4Plan plan_experts_host(int64_t pairs, const ql_w4_weight& w) {
   G4Plan g;
   const int64_t per = div_up(pairs, w.experts);
   g.splits = 1;
-  if (per > 64) {
-    g.rt = 2;
-    g.row_tiles = (unsigned)div_up(w.N, 256);
-    g.ntok = 128;
-  } else {
-    g.rt = 1;
-    g.row_tiles = (unsigned)div_up(w.N, 128);
-    g.ntok = per > 16 ? 64 : 32;
-  }
+  g.wide = per > 64;
+  g.row_tiles = (unsigned)div_up(w.N, g.wide ? 256 : 128);
+  g.ntok = g.wide ? kWideTok : per > 16 ? 64 : 32;
   g.tok_tiles = (unsigned)(std::min<int64_t>(w.experts, pairs) + pairs / g.ntok);
   return g;
 }
@@ -708,48 +1089,47 @@ G4Layout g4_layout(int64_t rows, int64_t K, int64_t pairs, unsigned tiles, int64
   return L;
 }
 
-template <int RT, int kGroup, bool kZero, bool kExperts>
-cudaError_t launch_g4_t(const CUtensorMap& tw, const CUtensorMap& tx, const G4Params& p, const G4Plan& g,
-                        cudaStream_t st) {
-  using Cfg = G4Cfg<RT>;
-  const int smem = 1024 + kG4WStages * Cfg::kWBytes + p.xstages * p.xstage +
-                   8 * (2 * kG4WStages + 2 * kG4MaxXStages + 2 * kG4Slots + 2) + 16 * Cfg::kTok + 16;
-  cudaError_t e = ensure_smem<w4_gemm_kernel<RT, kGroup, kZero, kExperts>>(smem);
+template <auto kKernel>
+cudaError_t launch_g4_kernel(const CUtensorMap& tw, const CUtensorMap& tx, const G4Params& p, dim3 grid, int threads,
+                             int smem, cudaStream_t st) {
+  cudaError_t e = ensure_smem<kKernel>(smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(g.row_tiles * g.splits, g.tok_tiles);
-  cfg.blockDim = dim3(kG4Threads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = g.splits;
+  attr[1].val.clusterDim.x = p.splits;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, w4_gemm_kernel<RT, kGroup, kZero, kExperts>, tw, tx, p);
+  return cudaLaunchKernelEx(&cfg, kKernel, tw, tx, p);
 }
 
-template <int RT, bool kExperts>
-cudaError_t launch_g4_group(const CUtensorMap& tw, const CUtensorMap& tx, const G4Params& p, const G4Plan& g,
-                            int group, cudaStream_t st) {
-  if (p.wz) {
-    if (group == 128) return launch_g4_t<RT, 128, true, kExperts>(tw, tx, p, g, st);
-    if (group == 64) return launch_g4_t<RT, 64, true, kExperts>(tw, tx, p, g, st);
-    return launch_g4_t<RT, 32, true, kExperts>(tw, tx, p, g, st);
+template <int kGroup, bool kZero, bool kExperts>
+cudaError_t launch_g4_t(const CUtensorMap& tw, const CUtensorMap& tx, const G4Params& p, const G4Plan& g, int sms,
+                        cudaStream_t st) {
+  const int ring = kG4WStages * (g.wide ? kWideWBytes : kNarrowWBytes) + p.xstages * p.xstage;
+  if (g.wide) {
+    const int smem = 1024 + ring + kWideEpiWarps * 16 * kWideStageRow + 32 * 8 + 4 * 256 * 4 + 8 * kWideTok * 4 + 16;
+    const unsigned grid = (unsigned)std::min<int64_t>(sms, (int64_t)g.row_tiles * g.tok_tiles);
+    return launch_g4_kernel<w4_wide_kernel<kGroup, kZero, kExperts>>(tw, tx, p, dim3(grid), kWideThreads, smem, st);
   }
-  if (group == 128) return launch_g4_t<RT, 128, false, kExperts>(tw, tx, p, g, st);
-  if (group == 64) return launch_g4_t<RT, 64, false, kExperts>(tw, tx, p, g, st);
-  return launch_g4_t<RT, 32, false, kExperts>(tw, tx, p, g, st);
+  const int smem = 1024 + ring + 8 * (2 * kG4WStages + 2 * kG4MaxXStages + 2 * kNarrowSlots + 2) + 16 * kNarrowTok + 16;
+  return launch_g4_kernel<w4_narrow_kernel<kGroup, kZero, kExperts>>(
+      tw, tx, p, dim3(g.row_tiles * g.splits, g.tok_tiles),
+      (kG4DequantWarps + (kExperts ? kG4Producers : 1) + 1) * 32, smem, st);
 }
 
 template <bool kExperts>
-cudaError_t launch_g4(const ql_w4_weight& w, const uint16_t* x16, int64_t rows, G4Params p, const G4Plan& g,
+cudaError_t launch_g4(const ql_w4_weight& w, const uint16_t* x16, int64_t rows, G4Params p, const G4Plan& g, int sms,
                       cudaStream_t st) {
-  if (g.tok_tiles > 65535u) return cudaErrorNotSupported;  // grid.y
+  if (g.tok_tiles > 65535u || (int64_t)g.tok_tiles * g.row_tiles >= (int64_t(1) << 31)) return cudaErrorNotSupported;
   CUtensorMap tw, tx;
   cudaError_t e = make_tmap_u8_sw128(&tw, w.wq, (uint64_t)w.K / 2, (uint64_t)w.experts * w.N, (uint64_t)w.K / 2, 128, 128);
   if (e != cudaSuccess) return e;
@@ -761,11 +1141,19 @@ cudaError_t launch_g4(const ql_w4_weight& w, const uint16_t* x16, int64_t rows, 
   p.K = w.K;
   p.groups = (int)div_up(w.K, w.group);
   p.ntok = g.ntok;
+  p.row_tiles = (int)g.row_tiles;
+  p.tok_tiles = (int)g.tok_tiles;
   p.xstage = (int)div_up(g.ntok * 128, 1024) * 1024;
   p.splits = g.splits;
-  p.xstages = std::min(kG4MaxXStages, std::max(3, (g.rt == 2 ? G4Cfg<2>::kRing : G4Cfg<1>::kRing) / p.xstage));
-  return g.rt == 2 ? launch_g4_group<2, kExperts>(tw, tx, p, g, (int)w.group, st)
-                   : launch_g4_group<1, kExperts>(tw, tx, p, g, (int)w.group, st);
+  p.xstages = std::min(kG4MaxXStages, std::max(3, (g.wide ? kWideRing : kNarrowRing) / p.xstage));
+  if (w.group == 128)
+    return w.wz ? launch_g4_t<128, true, kExperts>(tw, tx, p, g, sms, st)
+                : launch_g4_t<128, false, kExperts>(tw, tx, p, g, sms, st);
+  if (w.group == 64)
+    return w.wz ? launch_g4_t<64, true, kExperts>(tw, tx, p, g, sms, st)
+                : launch_g4_t<64, false, kExperts>(tw, tx, p, g, sms, st);
+  return w.wz ? launch_g4_t<32, true, kExperts>(tw, tx, p, g, sms, st)
+              : launch_g4_t<32, false, kExperts>(tw, tx, p, g, sms, st);
 }
 
 cudaError_t launch_pdl(void (*kernel)(const G4PrepParams), unsigned grid, unsigned block, const G4PrepParams& p,
@@ -811,7 +1199,7 @@ cudaError_t launch_w4(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint1
   p.ex = q.ex;
   p.M = M;
   p.status = status;
-  return launch_g4<false>(w, q.x16, M, p, g, st);
+  return launch_g4<false>(w, q.x16, M, p, g, sms, st);
 }
 
 size_t w4_experts_workspace_bytes(int64_t T, int64_t topk, const ql_w4_weight& w, bool combine, int sms) {
@@ -857,7 +1245,7 @@ cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float
   p.ntiles = q.ntiles;
   p.rows_per_token = combine ? 1 : (int)topk;
   p.status = status;
-  e = launch_g4<true>(w, q.x16, rows, p, g, st);
+  e = launch_g4<true>(w, q.x16, rows, p, g, sms, st);
   if (e != cudaSuccess || !combine) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)T, (unsigned)std::min<int64_t>(div_up(w.N, 128), 64));
