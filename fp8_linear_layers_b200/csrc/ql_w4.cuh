@@ -82,12 +82,21 @@ QL_DEVINL uint32_t f32x2_to_f16x2(float lo, float hi) {
   return r;
 }
 
-// Eight codes -> four f16 pairs (q - z) s in the order of codes_to_bf16.  A nibble in
-// bits 0-3 of f16 1024.0 reads as 1024 + q, one in bits 4-7 as 1024 + 16 q, so one
-// shift serves four pairs; zlo = (1024 + z) twice, zhi = -(64 + z) twice.  q - z is
-// exact; times s it is exact for z = 8 (at most 3 + 8 significant bits), and rounded
-// to 11 bits otherwise.
-QL_DEVINL void codes_to_f16(uint32_t w, uint32_t zlo, uint32_t zhi, uint32_t s, uint32_t* p) {
+// Eight codes -> four f16 pairs (q - 8) s in the order of codes_to_bf16.  A nibble in
+// bits 6-9 of f16 16.0 reads as 16 + q, so (q - 8) s = (16 + q) s - 24 s in one fma:
+// 24 s is exact (2 + 8 significant bits), and so is the result (at most 3 + 8).
+QL_DEVINL void codes_to_f16(uint32_t w, uint32_t s, uint32_t m24s, uint32_t* p) {
+  p[0] = fma_f16x2(and_or<0x03C003C0u, 0x4C004C00u>(w << 6), s, m24s);
+  p[1] = fma_f16x2(and_or<0x03C003C0u, 0x4C004C00u>(w << 2), s, m24s);
+  p[2] = fma_f16x2(and_or<0x03C003C0u, 0x4C004C00u>(w >> 2), s, m24s);
+  p[3] = fma_f16x2(and_or<0x03C003C0u, 0x4C004C00u>(w >> 6), s, m24s);
+}
+
+// With a zero point (16 + z) s may need 13 bits, so q - z comes first, exactly: a nibble
+// in bits 0-3 of f16 1024.0 reads as 1024 + q, one in bits 4-7 as 1024 + 16 q (one shift
+// serves four pairs); zlo = (1024 + z) twice, zhi = -(64 + z) twice.  The product with
+// s, up to 12 significant bits, is rounded to 11.
+QL_DEVINL void codes_to_f16_zero(uint32_t w, uint32_t zlo, uint32_t zhi, uint32_t s, uint32_t* p) {
   constexpr uint32_t kSixteenth = 0x2C002C00u;
   const uint32_t v = w >> 8;
   p[0] = mul_f16x2(sub_f16x2(and_or<0x000F000Fu, 0x64006400u>(w), zlo), s);
@@ -166,18 +175,6 @@ QL_DEVINL void ld16(uint32_t taddr, uint32_t (&r)[16]) {
 
 QL_DEVINL void ld1(uint32_t taddr, uint32_t (&r)[1]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr));
-}
-
-// Four rows of a row-major matrix by index, 128 bytes each from byte x, into 512
-// consecutive bytes (128-byte swizzle).  The map's box is one row high.
-QL_DEVINL void tma_gather4(uint32_t dst, const CUtensorMap* map, int32_t x, int4 rows, uint32_t bar,
-                           uint32_t elected) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %8, 0;\n\t"
-      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(dst),
-      "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar), "r"(elected)
-      : "memory");
 }
 
 // ---- clusters

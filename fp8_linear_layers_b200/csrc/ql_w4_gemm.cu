@@ -29,7 +29,6 @@ namespace ql {
 constexpr unsigned int KID_W4 = 4;  // KernelId of this file's GEMM in the device status word
 
 constexpr int kG4DequantWarps = 8;
-constexpr int kG4Producers = 3;  // warps that issue the token loads of experts (dense: one)
 constexpr int kG4StageK = 256;   // inputs of a weight stage (128 bytes of codes a row)
 constexpr int kG4GranK = 64;     // inputs of a token stage and of a TMEM weight slot
 constexpr int kG4WStages = 3;
@@ -37,13 +36,14 @@ constexpr int kG4MaxXStages = 8;
 constexpr int kG4PrepThreads = 128;
 constexpr int kG4PlanThreads = 1024;
 constexpr int kG4MaxSplit = 8;
+constexpr int64_t kG4CountPairs = 2048;  // experts: up to here each pair's place is counted by its own warp
 
 // Wide kernel: two 128-row weight tiles share up to 192 tokens; one CTA to an SM, which
 // takes tile after tile.  TMEM: 2 x 192 accumulator columns, 2 slots x 2 tiles x 32.
 constexpr int kWideTok = 192;
 constexpr int kWideRing = 110592;  // bytes of token stages
-constexpr int kWideFirstProducer = kG4DequantWarps;
-constexpr int kWideMma = kWideFirstProducer + kG4Producers;
+constexpr int kWideProducer = kG4DequantWarps;
+constexpr int kWideMma = kWideProducer + 1;
 constexpr int kWideFirstEpi = kWideMma + 1;
 constexpr int kWideEpiWarps = 8;
 constexpr int kWideThreads = (kWideFirstEpi + kWideEpiWarps) * 32;
@@ -55,6 +55,7 @@ constexpr int kWideWBytes = 2 * 128 * 128;
 constexpr int kNarrowTok = 128;
 constexpr int kNarrowRing = 57344;
 constexpr int kNarrowSlots = 4;
+constexpr int kNarrowThreads = (kG4DequantWarps + 2) * 32;
 constexpr int kNarrowWBytes = 128 * 128;
 
 struct G4Tile {
@@ -65,7 +66,7 @@ struct G4Params {
   const uint16_t* sw;
   const uint8_t* wz;
   uint16_t* y;           // dense, gather: the result; combine: the pairs' products
-  const int* ex;         // tokens' exponents
+  const int* ex;         // exponents of the prepared tokens (experts: of the sorted pairs)
   const int* order;      // experts: pairs sorted by expert
   const G4Tile* tiles;   // experts: token tiles
   const int* ntiles;
@@ -76,7 +77,6 @@ struct G4Params {
   int row_tiles, tok_tiles;  // wide, dense
   int xstage;            // bytes of a token stage
   int xstages;           // token stages
-  int rows_per_token;    // experts: pairs that share an x row (topk for gather, else 1)
   int splits;            // CTAs of a cluster along K
   DevStatus* status;
 };
@@ -118,7 +118,7 @@ template <int kGroup, bool kZero>
 struct G4Scales {
   static constexpr int kN = kG4StageK / kGroup;
   uint32_t sraw[kN], zraw[kZero ? kN : 1];
-  uint32_t s2[kN], zl[kZero ? kN : 1], zh[kZero ? kN : 1];
+  uint32_t s2[kN], z0[kN], z1[kZero ? kN : 1];  // kZero: zlo, zhi; else z0 = -24 s
 
   QL_DEVINL void load(const uint16_t* sw, const uint8_t* wz, int w, int groups) {
 #pragma unroll
@@ -134,48 +134,32 @@ struct G4Scales {
       const float s = scale2(__uint_as_float(sraw[i] << 16), f);
       s2[i] = w4::f32x2_to_f16x2(s, s);
       if constexpr (kZero) {
-        zl[i] = 0x64006400u + zraw[i] * 0x10001u;
+        z0[i] = 0x64006400u + zraw[i] * 0x10001u;
         const float zf = -(64.0f + (float)zraw[i]);
-        zh[i] = w4::f32x2_to_f16x2(zf, zf);
+        z1[i] = w4::f32x2_to_f16x2(zf, zf);
+      } else {
+        z0[i] = w4::f32x2_to_f16x2(-24.0f * s, -24.0f * s);
       }
     }
   }
-  // 64 inputs, granule gq of the stage, from this row's 128 swizzled bytes.
-  QL_DEVINL void granule(const uint8_t* row, int gq, uint32_t rsw, uint32_t (&h)[32]) const {
+  // A row's 32 bytes of codes of granule gq, from the row's 128 swizzled bytes.
+  static QL_DEVINL void codes(const uint8_t* row, int gq, uint32_t rsw, uint32_t (&c)[8]) {
     const uint4 c0 = *reinterpret_cast<const uint4*>(row + (((uint32_t)(2 * gq) ^ rsw) << 4));
     const uint4 c1 = *reinterpret_cast<const uint4*>(row + (((uint32_t)(2 * gq + 1) ^ rsw) << 4));
-    const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w;
+    c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
+  }
+  QL_DEVINL void granule(const uint32_t (&c)[8], int gq, uint32_t (&h)[32]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int gi = (gq * 64 + i * 8) / kGroup;
       if constexpr (kZero)
-        w4::codes_to_f16(c[i], zl[gi], zh[gi], s2[gi], h + 4 * i);
+        w4::codes_to_f16_zero(c[i], z0[gi], z1[gi], s2[gi], h + 4 * i);
       else
-        w4::codes_to_f16(c[i], 0x64086408u, 0xD480D480u, s2[gi], h + 4 * i);  // 1032, -72
+        w4::codes_to_f16(c[i], s2[gi], z0[gi], h + 4 * i);
     }
   }
 };
-
-// One granule of tokens to a stage: dense, a box of the token matrix; experts, this
-// producer warp's share of the gathered rows.
-template <bool kExperts>
-QL_DEVINL void load_tokens(const CUtensorMap& tmX, uint8_t* dst, uint64_t* bar, uint32_t bytes, int xb, int m0,
-                           const int* rows, int count, int pw, int lane, uint64_t policy) {
-  if constexpr (kExperts) {
-    if (pw == 0 && lane == 0) mbar_arrive_expect_tx(bar, bytes);
-    __syncwarp();
-    const uint32_t elected = w4::elect_one();
-    const uint32_t d = smem_u32(dst), b = smem_u32(bar);
-    for (int i = 4 * pw; i < count; i += 4 * kG4Producers)
-      w4::tma_gather4(d + i * 128, &tmX, xb, *reinterpret_cast<const int4*>(rows + i), b, elected);
-  } else {
-    if (lane == 0) {
-      mbar_arrive_expect_tx(bar, bytes);
-      tc::tma_load_2d(dst, &tmX, xb, m0, bar, policy);
-    }
-  }
-  __syncwarp();
-}
 
 // What the K range of a CTA looks like: weight stages [w0, w0 + n), taken in rotated
 // order.  The CTAs start at different stages: marching through K together they would
@@ -193,12 +177,11 @@ struct G4Range {
 // ---------------------------------------------------------------------------- narrow
 
 template <int kGroup, bool kZero, bool kExperts>
-__global__ void __launch_bounds__((kG4DequantWarps + (kExperts ? kG4Producers : 1) + 1) * 32, 2)
+__global__ void __launch_bounds__(kNarrowThreads, 2)
     w4_narrow_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                      const G4Params p) {
-  constexpr int kProducers = kExperts ? kG4Producers : 1;
-  constexpr int kMmaWarp = kG4DequantWarps + kProducers;
-  constexpr int kThreads = (kMmaWarp + 1) * 32;
+  constexpr int kMmaWarp = kG4DequantWarps + 1;
+  constexpr int kThreads = kNarrowThreads;
   constexpr int kSlots = kNarrowSlots;
   const int xs_n = p.xstages;
   extern __shared__ uint8_t smem_raw[];
@@ -212,8 +195,7 @@ __global__ void __launch_bounds__((kG4DequantWarps + (kExperts ? kG4Producers : 
   uint64_t* aempty = afull + kSlots;
   uint64_t* done = aempty + kSlots;
   int* s_ex = reinterpret_cast<int*>(done + 2);               // the columns' exponents (16-byte aligned)
-  int* s_row = s_ex + kNarrowTok;                              // experts: x rows
-  int* s_out = s_row + kNarrowTok;                             // experts: pairs
+  int* s_out = s_ex + kNarrowTok;                              // experts: pairs
   float* s_fac = reinterpret_cast<float*>(s_out + kNarrowTok); // 2^-exponent
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_fac + kNarrowTok);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
@@ -265,25 +247,17 @@ __global__ void __launch_bounds__((kG4DequantWarps + (kExperts ? kG4Producers : 
     const G4Tile tile = live ? p.tiles[blockIdx.y] : G4Tile{0, 0, 0, 0};
     e = tile.expert;
     count = tile.count;
-    for (int i = threadIdx.x; i < p.ntok && count > 0; i += kThreads) {
-      const int pair = p.order[tile.start + min(i, count - 1)];
-      const int row = pair / p.rows_per_token;
-      const int ex = p.ex[row];
-      s_out[i] = pair;
-      s_row[i] = row;
-      s_ex[i] = ex;
-      s_fac[i] = exp2i(max(-126, min(126, -ex)));
-      if (abs(ex) > 60) *s_wide = 1;
-    }
+    m0 = tile.start;
   } else {
     m0 = (int64_t)blockIdx.y * p.ntok;
     count = (int)min((int64_t)p.ntok, p.M - m0);
-    for (int i = threadIdx.x; i < count; i += kThreads) {
-      const int ex = p.ex[m0 + i];
-      s_ex[i] = ex;
-      s_fac[i] = exp2i(max(-126, min(126, -ex)));
-      if (abs(ex) > 60) *s_wide = 1;
-    }
+  }
+  for (int i = threadIdx.x; i < count; i += kThreads) {
+    const int ex = p.ex[m0 + i];
+    if constexpr (kExperts) s_out[i] = p.order[m0 + i];
+    s_ex[i] = ex;
+    s_fac[i] = exp2i(max(-126, min(126, -ex)));
+    if (abs(ex) > 60) *s_wide = 1;
   }
   tc::fence_before();
   __syncthreads();
@@ -292,34 +266,33 @@ __global__ void __launch_bounds__((kG4DequantWarps + (kExperts ? kG4Producers : 
   const uint32_t tmem_a = tmem + 128;
   const int mma_n = (count + 15) & ~15;
 
-  if (count > 0 && warp >= kG4DequantWarps && warp < kMmaWarp) {
-    // ------------------------------------------------------------ TMA producers
-    const int pw = warp - kG4DequantWarps;
+  if (count > 0 && warp == kG4DequantWarps) {
+    // ------------------------------------------------------------ TMA producer
     const uint64_t pol_w = l2_policy_evict_first();
     const uint64_t pol_x = l2_policy_evict_last();
     const int wrow = (int)(e * p.N + n0);
-    const uint32_t xbytes = kExperts ? (uint32_t)((count + 3) / 4) * 512u : (uint32_t)p.ntok * 128u;
     bool ok = true;
     int jw = 0, jx = 0;  // issued stages
     int s = 0;           // token stage of the next granule, and how often it was filled
     uint32_t fill = 0;
     for (; jw < kr.n && ok; ++jw) {
       const int v = jw % kG4WStages, w = kr.stage(jw);
-      if (pw == 0) {
-        if (jw >= kG4WStages) ok = w4::wait(&wempty[v], ((jw / kG4WStages) - 1) & 1, abort_flag);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&wfull[v], kNarrowWBytes);
-          tc::tma_load_2d(wring + v * kNarrowWBytes, &tmW, w * 128, wrow, &wfull[v], pol_w);
-        }
-        __syncwarp();
+      if (jw >= kG4WStages) ok = w4::wait(&wempty[v], ((jw / kG4WStages) - 1) & 1, abort_flag);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&wfull[v], kNarrowWBytes);
+        tc::tma_load_2d(wring + v * kNarrowWBytes, &tmW, w * 128, wrow, &wfull[v], pol_w);
       }
+      __syncwarp();
       const int ng = kr.granules(w);
       for (int gq = 0; gq < ng; ++gq) {
         if (fill > 0) ok = w4::wait(&xempty[s], (fill - 1) & 1, abort_flag);
         if (!ok) break;
-        load_tokens<kExperts>(tmX, xring + s * p.xstage, &xfull[s], xbytes, (w * 4 + gq) * 128, (int)m0, s_row,
-                              count, pw, lane, pol_x);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&xfull[s], (uint32_t)p.ntok * 128u);
+          tc::tma_load_2d(xring + s * p.xstage, &tmX, (w * 4 + gq) * 128, (int)m0, &xfull[s], pol_x);
+        }
+        __syncwarp();
         ++jx;
         if (++s == xs_n) {
           s = 0;
@@ -330,8 +303,8 @@ __global__ void __launch_bounds__((kG4DequantWarps + (kExperts ? kG4Producers : 
     if (!ok) {
       if (lane == 0 && !*abort_flag) record_timeout(p.status, KID_W4, 1);
       *abort_flag = 1;
-      // the copies in flight land before the CTA leaves
-      for (int j = max(0, jw - kG4WStages); j < jw && pw == 0; ++j)
+      // the copies in flight land before the CTA leaves (step jw's weights may be among them)
+      for (int j = max(0, jw - kG4WStages + 1); j < min(jw + 1, kr.n); ++j)
         mbar_wait_bounded(&wfull[j % kG4WStages], (j / kG4WStages) & 1, nullptr);
       for (int j = max(0, jx - xs_n); j < jx; ++j) mbar_wait_bounded(&xfull[j % xs_n], (j / xs_n) & 1, nullptr);
     }
@@ -394,8 +367,9 @@ __global__ void __launch_bounds__((kG4DequantWarps + (kExperts ? kG4Producers : 
       for (int gq = 0; gq < 4; ++gq, ++j) {
         if (gq >= ng) break;
         if ((j & 1) != wg) continue;
-        uint32_t h[32];
-        sc.granule(src, gq, (uint32_t)(lane & 7), h);
+        uint32_t c[8], h[32];
+        sc.codes(src, gq, (uint32_t)(lane & 7), c);
+        sc.granule(c, gq, h);
         const int slot = j % kSlots, use = j / kSlots;
         if (use > 0) ok = w4::wait(&aempty[slot], (use - 1) & 1, abort_flag);
         if (!ok) break;
@@ -434,11 +408,12 @@ __global__ void __launch_bounds__((kG4DequantWarps + (kExperts ? kG4Producers : 
         uint32_t v[16];
         w4::ld16(tmem + lane_addr + c, v);
         tc::ld_wait();
+        if (!wide) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float acc = __uint_as_float(v[i]);
-          // wide: the two factors may leave f32's range where their product does not
-          o[i] = !wide ? acc * rf * s_fac[c + i] : c + i < count ? scale2(acc, -(f + s_ex[c + i])) : 0.0f;
+          for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(v[i]) * rf * s_fac[c + i];
+        } else {  // the two factors may leave f32's range where their product does not
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = scale2(__uint_as_float(v[i]), -(f + (c + i < count ? s_ex[c + i] : 0)));
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -507,8 +482,8 @@ __global__ void __launch_bounds__((kG4DequantWarps + (kExperts ? kG4Producers : 
 
 // One tile of the persistent kernel: a row tile of 256 weights and up to ntok tokens.
 struct WideTile {
-  int64_t e, m0;
-  int start, count, rt, tt;
+  int64_t e, m0;  // expert; first token row
+  int count, rt, tt;
 };
 
 template <bool kExperts>
@@ -519,12 +494,10 @@ QL_DEVINL WideTile wide_tile(const G4Params& p, int t) {
   if constexpr (kExperts) {
     const G4Tile g = p.tiles[w.tt];
     w.e = g.expert;
-    w.start = g.start;
+    w.m0 = g.start;
     w.count = g.count;
-    w.m0 = 0;
   } else {
     w.e = 0;
-    w.start = 0;
     w.m0 = (int64_t)w.tt * p.ntok;
     w.count = (int)min((int64_t)p.ntok, p.M - w.m0);
   }
@@ -562,8 +535,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   // [4][256] the rows' exponents: with short K the dequantizing warps are up to three
   // tiles ahead of the epilogue
   int* s_f = reinterpret_cast<int*>(wfull + 32);
-  int* s_row = s_f + 4 * 256;                                     // [2][kWideTok] experts: x rows
-  int* s_out = s_row + 2 * kWideTok;                              // [2][kWideTok] experts: pairs
+  int* s_out = s_f + 4 * 256;                                     // [2][kWideTok] experts: pairs
   int* s_ex = s_out + 2 * kWideTok;                               // [2][kWideTok] the columns' exponents
   float* s_fac = reinterpret_cast<float*>(s_ex + 2 * kWideTok);   // [2][kWideTok] 2^-exponent
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_fac + 2 * kWideTok);
@@ -609,44 +581,37 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int tiles = p.row_tiles * (kExperts ? *p.ntiles : p.tok_tiles);
   bool ok = true;
 
-  if (warp >= kWideFirstProducer && warp < kWideMma) {
-    // ------------------------------------------------------------ TMA producers
-    const int pw = warp - kWideFirstProducer;
+  if (warp == kWideProducer) {
+    // ------------------------------------------------------------ TMA producer
     const uint64_t pol_w = l2_policy_evict_first();
     const uint64_t pol_x = l2_policy_evict_last();
     int jw = 0, jx = 0;  // issued stages
     int s = 0;           // token stage of the next granule, and how often it was filled
     uint32_t fill = 0;
-    int it = 0;
-    for (int t = blockIdx.x; t < tiles && ok && (kExperts || pw == 0); t += gridDim.x, ++it) {
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const WideTile w = wide_tile<kExperts>(p, t);
       kr.rot = (w.rt * 5 + w.tt * 3) % kr.n;
-      const int* rows = s_row + (it & 1) * kWideTok;
-      if constexpr (kExperts) {
-        for (int i = threadIdx.x - kWideFirstProducer * 32; i < ((w.count + 3) & ~3); i += kG4Producers * 32)
-          s_row[(it & 1) * kWideTok + i] = p.order[w.start + min(i, w.count - 1)] / p.rows_per_token;
-        named_bar_sync(2, kG4Producers * 32);
-      }
       const int wrow = (int)(w.e * p.N + (int64_t)w.rt * 256);
-      const uint32_t xbytes = kExperts ? (uint32_t)((w.count + 3) / 4) * 512u : (uint32_t)p.ntok * 128u;
-      for (int j = 0; j < kr.n && ok; ++j, ++jw) {
+      for (int j = 0; j < kr.n && ok; ++j) {
         const int v = jw % kG4WStages, ws = kr.stage(j);
-        if (pw == 0) {
-          if (jw >= kG4WStages) ok = w4::wait(&wempty[v], ((jw / kG4WStages) - 1) & 1, abort_flag);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&wfull[v], kWideWBytes);
-            tc::tma_load_2d(wring + v * kWideWBytes, &tmW, ws * 128, wrow, &wfull[v], pol_w);
-            tc::tma_load_2d(wring + v * kWideWBytes + 16384, &tmW, ws * 128, wrow + 128, &wfull[v], pol_w);
-          }
-          __syncwarp();
+        if (jw >= kG4WStages) ok = w4::wait(&wempty[v], ((jw / kG4WStages) - 1) & 1, abort_flag);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&wfull[v], kWideWBytes);
+          tc::tma_load_2d(wring + v * kWideWBytes, &tmW, ws * 128, wrow, &wfull[v], pol_w);
+          tc::tma_load_2d(wring + v * kWideWBytes + 16384, &tmW, ws * 128, wrow + 128, &wfull[v], pol_w);
         }
+        __syncwarp();
+        ++jw;
         const int ng = kr.granules(ws);
         for (int gq = 0; gq < ng; ++gq) {
           if (fill > 0) ok = w4::wait(&xempty[s], (fill - 1) & 1, abort_flag);
           if (!ok) break;
-          load_tokens<kExperts>(tmX, xring + s * p.xstage, &xfull[s], xbytes, (ws * 4 + gq) * 128, (int)w.m0, rows,
-                                w.count, pw, lane, pol_x);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&xfull[s], (uint32_t)p.ntok * 128u);
+            tc::tma_load_2d(xring + s * p.xstage, &tmX, (ws * 4 + gq) * 128, (int)w.m0, &xfull[s], pol_x);
+          }
+          __syncwarp();
           ++jx;
           if (++s == xs_n) {
             s = 0;
@@ -659,7 +624,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (lane == 0 && !*abort_flag) record_timeout(p.status, KID_W4, 4);
       *abort_flag = 1;
       // the copies in flight land before the CTA leaves
-      for (int j = max(0, jw - kG4WStages); j < jw && pw == 0; ++j)
+      for (int j = max(0, jw - kG4WStages); j < jw; ++j)
         mbar_wait_bounded(&wfull[j % kG4WStages], (j / kG4WStages) & 1, nullptr);
       for (int j = max(0, jx - xs_n); j < jx; ++j) mbar_wait_bounded(&xfull[j % xs_n], (j / xs_n) & 1, nullptr);
     }
@@ -729,11 +694,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         ok = w4::wait(&wfull[ws], (jw / kG4WStages) & 1, abort_flag);
         if (!ok) break;
         const uint8_t* src = wring + ws * kWideWBytes + row * 128;
+        uint32_t c[8];
+        sc.codes(src, 0, (uint32_t)(lane & 7), c);
 #pragma unroll
         for (int gq = 0; gq < 4; ++gq) {
           if (gq >= ng) break;
           uint32_t h[32];
-          sc.granule(src, gq, (uint32_t)(lane & 7), h);
+          sc.granule(c, gq, h);
+          if (gq < 3) sc.codes(src, gq + 1, (uint32_t)(lane & 7), c);
           const int slot = g & 1, use = g >> 1;
           if (use > 0) ok = w4::wait(&aempty[slot], (use - 1) & 1, abort_flag);
           if (!ok) break;
@@ -769,13 +737,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const int buf = (it & 1) * kWideTok;
       bool wide = false;
       if (et < w.count) {
-        int64_t xrow = w.m0 + et;
-        if constexpr (kExperts) {
-          const int pair = p.order[w.start + et];
-          s_out[buf + et] = pair;
-          xrow = pair / p.rows_per_token;
-        }
-        const int ex = p.ex[xrow];
+        const int ex = p.ex[w.m0 + et];
+        if constexpr (kExperts) s_out[buf + et] = p.order[w.m0 + et];
         s_ex[buf + et] = ex;
         s_fac[buf + et] = exp2i(max(-126, min(126, -ex)));
         wide = abs(ex) > 60;
@@ -789,6 +752,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       wide = __any_sync(0xffffffffu, wide || abs(f) > 60);
       const float rf = exp2i(max(-126, min(126, -f)));
       const int64_t nw = (int64_t)w.rt * 256 + r * 128 + q * 32;  // the warp's first output
+      uint16_t* yb = p.y + nw + (lane & 3) * 8;                    // this lane's piece of an output row
+      const bool inside = nw + (lane & 3) * 8 < p.N;
+      const uint8_t* src = stg + (lane >> 2) * kWideStageRow + (lane & 3) * 16;
       const int mma_n = (w.count + 15) & ~15;
       for (int c = 0; c < mma_n; c += 16) {
         uint32_t v[16];
@@ -800,12 +766,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (lane == 0) mbar_arrive(dempty);
         }
         float o[16];
+        if (!wide) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float acc = __uint_as_float(v[i]);
-          // wide: the two factors may leave f32's range where their product does not
-          o[i] = !wide ? acc * rf * s_fac[buf + c + i]
-                       : c + i < w.count ? scale2(acc, -(f + s_ex[buf + c + i])) : 0.0f;
+          for (int i = 0; i < 16; i += 4) {
+            const float4 fac = *reinterpret_cast<const float4*>(s_fac + buf + c + i);
+            o[i] = __uint_as_float(v[i]) * rf * fac.x;
+            o[i + 1] = __uint_as_float(v[i + 1]) * rf * fac.y;
+            o[i + 2] = __uint_as_float(v[i + 2]) * rf * fac.z;
+            o[i + 3] = __uint_as_float(v[i + 3]) * rf * fac.w;
+          }
+        } else {  // the two factors may leave f32's range where their product does not
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = scale2(__uint_as_float(v[i]), -(f + (c + i < w.count ? s_ex[buf + c + i] : 0)));
         }
         if (vec) {
 #pragma unroll
@@ -814,12 +786,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int tok = h * 8 + (lane >> 2), piece = lane & 3;
-            const int64_t n = nw + piece * 8;
-            if (c + tok < w.count && n < p.N) {
-              const int64_t orow = kExperts ? s_out[buf + c + tok] : w.m0 + c + tok;
-              *reinterpret_cast<uint4*>(p.y + orow * p.N + n) =
-                  *reinterpret_cast<const uint4*>(stg + tok * kWideStageRow + piece * 16);
+            const int tok = c + h * 8 + (lane >> 2);
+            if (tok < w.count && inside) {
+              uint16_t* out = kExperts ? yb + s_out[buf + tok] * p.N : yb + (w.m0 + tok) * p.N;
+              *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(src + h * 8 * kWideStageRow);
             }
           }
           __syncwarp();
@@ -853,33 +823,33 @@ struct G4PrepParams {
   const uint16_t* x;
   uint16_t* x16;
   int* ex;
-  int64_t rows, K;
+  int64_t K;
   // experts
   const int32_t* ids;
   int64_t pairs;
-  int E, ntok, topk;
-  int* order;
+  int E, ntok;
+  int slots;             // pairs of an x row: topk (gather) or 1 (combine)
+  int* order;            // [pairs] the pairs by expert
+  int* pos;              // [pairs] many pairs: their places in `order` (-1: id out of range); else null
   G4Tile* tiles;
   int* ntiles;
-  uint16_t* zero_y;  // gather: the result, whose rows of an id out of range are zeroed
+  uint16_t* zero_y;      // gather: the result, whose rows of an id out of range are zeroed
   int64_t N;
 };
 
-// Block 0 of an experts launch: the pairs in expert order and the token tiles.  The
-// order inside an expert depends on timing; results do not, since a pair is one MMA
-// column wherever it stands.
-QL_DEVINL void plan_experts(const G4PrepParams& p, int* hist) {
-  int* base = hist + 1024;
+// Cuts the experts' pairs, in expert order, into token tiles; one thread per expert.
+// Returns the first place of expert threadIdx.x's pairs.
+QL_DEVINL int plan_tiles(const G4PrepParams& p, int* hist) {
   __shared__ int warp_sums[2][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < 1024; i += kG4PlanThreads) hist[i] = 0;
+  hist[tid] = 0;
   __syncthreads();
   for (int64_t i = tid; i < p.pairs; i += kG4PlanThreads) {
     const int e = p.ids[i];
     if (e >= 0 && e < p.E) atomicAdd(&hist[e], 1);
   }
   __syncthreads();
-  // exclusive sums of the pairs and of the tiles; one thread per expert
+  // exclusive sums of the pairs and of the tiles
   const int c = hist[tid], t = (c + p.ntok - 1) / p.ntok;
   int ci = c, ti = t;
 #pragma unroll
@@ -913,24 +883,33 @@ QL_DEVINL void plan_experts(const G4PrepParams& p, int* hist) {
     ci += warp_sums[0][warp - 1];
     ti += warp_sums[1][warp - 1];
   }
-  base[tid] = ci - c;
   const int per = t ? ((c + t - 1) / t + 15) & ~15 : 0;  // an expert's tiles are alike
   for (int i = 0; i < t; ++i) p.tiles[ti - t + i] = G4Tile{tid, ci - c + i * per, min(per, c - i * per), 0};
   if (tid == kG4PlanThreads - 1) *p.ntiles = ti;
+  return ci - c;
+}
+
+// Many pairs: one block plans and gives every pair its place.  The order inside an
+// expert depends on timing; results do not, since a pair is one MMA column wherever it
+// stands.
+__global__ void __launch_bounds__(kG4PlanThreads) w4_plan_kernel(const G4PrepParams p) {
+  __shared__ int hist[kG4PlanThreads];
+  tc::grid_dependency_wait();
+  tc::launch_dependents();
+  const int base = plan_tiles(p, hist);
   __syncthreads();
-  for (int64_t i = tid; i < p.pairs; i += kG4PlanThreads) {
+  hist[threadIdx.x] = base;
+  __syncthreads();
+  for (int64_t i = threadIdx.x; i < p.pairs; i += kG4PlanThreads) {
     const int e = p.ids[i];
-    if (e >= 0 && e < p.E) p.order[atomicAdd(&base[e], 1)] = (int)i;
+    p.pos[i] = e >= 0 && e < p.E ? atomicAdd(&hist[e], 1) : -1;
   }
 }
 
-// One row of tokens: the exponent of its largest finite |x| and the scaled f16 values.
-QL_DEVINL void prepare_row(const G4PrepParams& p, int64_t row, int tid, int threads, float* red) {
-  const uint4* src = reinterpret_cast<const uint4*>(p.x + row * p.K);
-  uint4* dst = reinterpret_cast<uint4*>(p.x16 + row * p.K);
-  const int chunks = (int)(p.K / 8);
+// The power of two of a row of tokens: its largest finite |x| to [2^14, 2^15).
+QL_DEVINL int token_exponent(const uint4* src, int chunks, uint32_t* red) {
   uint32_t top = 0;
-  for (int i = tid; i < chunks; i += threads) {
+  for (int i = threadIdx.x; i < chunks; i += blockDim.x) {
     const uint4 v = __ldg(src + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -941,53 +920,89 @@ QL_DEVINL void prepare_row(const G4PrepParams& p, int64_t row, int tid, int thre
     }
   }
   top = __reduce_max_sync(0xffffffffu, top);
-  uint32_t* r = reinterpret_cast<uint32_t*>(red);
-  if ((tid & 31) == 0) r[tid >> 5] = top;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
   __syncthreads();
   top = 0;
-  for (int i = 0; i < threads / 32; ++i) top = max(top, r[i]);
-  const int e = 14 - log2_bf16(top, 14);
-  if (tid == 0) p.ex[row] = e;
-  const float f0 = exp2i(e / 2), f1 = exp2i(e - e / 2);
-  for (int i = tid; i < chunks; i += threads) {
-    const uint4 v = __ldg(src + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float x[8];
+  for (int i = 0; i < (int)blockDim.x / 32; ++i) top = max(top, red[i]);
+  return 14 - log2_bf16(top, 14);
+}
+
+// Eight inputs scaled by f0 f1, in the order 0 4 1 5 2 6 3 7.
+QL_DEVINL uint4 prepare8(const uint4& v, float f0, float f1) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float x[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = bf16_lo(w[j]) * f0 * f1;
-      x[2 * j + 1] = bf16_hi(w[j]) * f0 * f1;
-    }
-    dst[i] = make_uint4(w4::f32x2_to_f16x2(x[0], x[4]), w4::f32x2_to_f16x2(x[1], x[5]),
-                        w4::f32x2_to_f16x2(x[2], x[6]), w4::f32x2_to_f16x2(x[3], x[7]));
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = bf16_lo(w[j]) * f0 * f1;
+    x[2 * j + 1] = bf16_hi(w[j]) * f0 * f1;
   }
+  return make_uint4(w4::f32x2_to_f16x2(x[0], x[4]), w4::f32x2_to_f16x2(x[1], x[5]),
+                    w4::f32x2_to_f16x2(x[2], x[6]), w4::f32x2_to_f16x2(x[3], x[7]));
 }
 
 __global__ void __launch_bounds__(kG4PrepThreads) w4_prepare_kernel(const G4PrepParams p) {
-  __shared__ float red[32];
+  __shared__ uint32_t red[32];
   tc::grid_dependency_wait();
   tc::launch_dependents();
-  prepare_row(p, blockIdx.x, threadIdx.x, kG4PrepThreads, red);
+  const int64_t row = blockIdx.x;
+  const uint4* src = reinterpret_cast<const uint4*>(p.x + row * p.K);
+  const int chunks = (int)(p.K / 8);
+  const int e = token_exponent(src, chunks, red);
+  if (threadIdx.x == 0) p.ex[row] = e;
+  const float f0 = exp2i(e / 2), f1 = exp2i(e - e / 2);
+  uint4* dst = reinterpret_cast<uint4*>(p.x16 + row * p.K);
+  for (int i = threadIdx.x; i < chunks; i += kG4PrepThreads) dst[i] = prepare8(__ldg(src + i), f0, f1);
 }
 
-// Experts: block 0 plans, the others take eight groups of 128 threads' rows in turn.
+// Experts: a block takes an x row and writes it once for each of its pairs, in expert
+// order, so that a tile's tokens are one box for TMA.  (Gathering them in the product
+// instead, with TMA's gather of four rows or with 16-byte asynchronous copies, took 1100
+// and 1700 cycles for a granule of 170 tokens whose MMAs take 680.)  Few pairs: every
+// warp counts its pair's place itself, and block 0 plans the tiles beside the others.
 __global__ void __launch_bounds__(kG4PlanThreads) w4_prepare_experts_kernel(const G4PrepParams p) {
-  __shared__ int hist[2048];
+  __shared__ int hist[kG4PlanThreads];
+  __shared__ uint32_t red[32];
+  __shared__ int s_pos[32];
   tc::grid_dependency_wait();
   tc::launch_dependents();
-  if (blockIdx.x == 0) {
-    plan_experts(p, hist);
-    return;
-  }
-  for (int64_t row = blockIdx.x - 1; row < p.rows; row += gridDim.x - 1) {
-    prepare_row(p, row, threadIdx.x, kG4PlanThreads, reinterpret_cast<float*>(hist));
-    __syncthreads();
-    if (p.zero_y) {
-      for (int j = 0; j < p.topk; ++j) {
-        const int e = p.ids[row * p.topk + j];
-        if (e >= 0 && e < p.E) continue;
-        for (int64_t n = threadIdx.x; n < p.N; n += kG4PlanThreads) p.zero_y[(row * p.topk + j) * p.N + n] = 0;
+  int64_t row = blockIdx.x;
+  if (!p.pos) {
+    if (row == 0) {
+      plan_tiles(p, hist);
+      return;
+    }
+    --row;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int j = warp; j < p.slots; j += blockDim.x / 32) {
+      const int pair = (int)row * p.slots + j, e = p.ids[pair];
+      int before = 0;
+      for (int i = lane; i < (int)p.pairs; i += 32) {
+        const int o = p.ids[i];
+        before += (o >= 0 && o < e) || (o == e && i < pair);
       }
+      before = __reduce_add_sync(0xffffffffu, before);
+      if (lane == 0) s_pos[j] = e >= 0 && e < p.E ? before : -1;
+    }
+  } else if (threadIdx.x < p.slots) {
+    s_pos[threadIdx.x] = p.pos[row * p.slots + threadIdx.x];
+  }
+  const uint4* src = reinterpret_cast<const uint4*>(p.x + row * p.K);
+  const int chunks = (int)(p.K / 8);
+  const int e = token_exponent(src, chunks, red);  // (and a barrier behind s_pos)
+  const float f0 = exp2i(e / 2), f1 = exp2i(e - e / 2);
+  if (threadIdx.x < p.slots && s_pos[threadIdx.x] >= 0) {
+    p.ex[s_pos[threadIdx.x]] = e;
+    p.order[s_pos[threadIdx.x]] = (int)row * p.slots + threadIdx.x;
+  }
+  for (int i = threadIdx.x; i < chunks; i += blockDim.x) {
+    const uint4 v = prepare8(__ldg(src + i), f0, f1);
+    for (int j = 0; j < p.slots; ++j)
+      if (s_pos[j] >= 0) reinterpret_cast<uint4*>(p.x16 + (int64_t)s_pos[j] * p.K)[i] = v;
+  }
+  if (p.zero_y) {
+    for (int j = 0; j < p.slots; ++j) {
+      if (s_pos[j] >= 0) continue;
+      for (int64_t n = threadIdx.x; n < p.N; n += blockDim.x) p.zero_y[(row * p.slots + j) * p.N + n] = 0;
     }
   }
 }
@@ -1065,7 +1080,7 @@ G4Plan plan_experts_host(int64_t pairs, const ql_w4_weight& w) {
 }
 
 struct G4Layout {
-  size_t x16, ex, order, tiles, ntiles, yp, total;
+  size_t x16, ex, order, pos, tiles, ntiles, yp, total;
 };
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -1078,6 +1093,8 @@ G4Layout g4_layout(int64_t rows, int64_t K, int64_t pairs, unsigned tiles, int64
   L.ex = off;
   off += up256((size_t)rows * 4);
   L.order = off;
+  off += up256((size_t)pairs * 4);
+  L.pos = off;
   off += up256((size_t)pairs * 4);
   L.tiles = off;
   off += up256((size_t)tiles * sizeof(G4Tile));
@@ -1116,14 +1133,13 @@ cudaError_t launch_g4_t(const CUtensorMap& tw, const CUtensorMap& tx, const G4Pa
                         cudaStream_t st) {
   const int ring = kG4WStages * (g.wide ? kWideWBytes : kNarrowWBytes) + p.xstages * p.xstage;
   if (g.wide) {
-    const int smem = 1024 + ring + kWideEpiWarps * 16 * kWideStageRow + 32 * 8 + 4 * 256 * 4 + 8 * kWideTok * 4 + 16;
+    const int smem = 1024 + ring + kWideEpiWarps * 16 * kWideStageRow + 32 * 8 + 4 * 256 * 4 + 6 * kWideTok * 4 + 16;
     const unsigned grid = (unsigned)std::min<int64_t>(sms, (int64_t)g.row_tiles * g.tok_tiles);
     return launch_g4_kernel<w4_wide_kernel<kGroup, kZero, kExperts>>(tw, tx, p, dim3(grid), kWideThreads, smem, st);
   }
-  const int smem = 1024 + ring + 8 * (2 * kG4WStages + 2 * kG4MaxXStages + 2 * kNarrowSlots + 2) + 16 * kNarrowTok + 16;
+  const int smem = 1024 + ring + 8 * (2 * kG4WStages + 2 * kG4MaxXStages + 2 * kNarrowSlots + 2) + 12 * kNarrowTok + 16;
   return launch_g4_kernel<w4_narrow_kernel<kGroup, kZero, kExperts>>(
-      tw, tx, p, dim3(g.row_tiles * g.splits, g.tok_tiles),
-      (kG4DequantWarps + (kExperts ? kG4Producers : 1) + 1) * 32, smem, st);
+      tw, tx, p, dim3(g.row_tiles * g.splits, g.tok_tiles), kNarrowThreads, smem, st);
 }
 
 template <bool kExperts>
@@ -1133,7 +1149,7 @@ cudaError_t launch_g4(const ql_w4_weight& w, const uint16_t* x16, int64_t rows, 
   CUtensorMap tw, tx;
   cudaError_t e = make_tmap_u8_sw128(&tw, w.wq, (uint64_t)w.K / 2, (uint64_t)w.experts * w.N, (uint64_t)w.K / 2, 128, 128);
   if (e != cudaSuccess) return e;
-  e = make_tmap_u8_sw128(&tx, x16, (uint64_t)w.K * 2, (uint64_t)rows, (uint64_t)w.K * 2, 128, kExperts ? 1 : g.ntok);
+  e = make_tmap_u8_sw128(&tx, x16, (uint64_t)w.K * 2, (uint64_t)rows, (uint64_t)w.K * 2, 128, g.ntok);
   if (e != cudaSuccess) return e;
   p.sw = w.sw;
   p.wz = w.wz;
@@ -1190,7 +1206,6 @@ cudaError_t launch_w4(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint1
   q.x = x;
   q.x16 = reinterpret_cast<uint16_t*>(ws + L.x16);
   q.ex = reinterpret_cast<int*>(ws + L.ex);
-  q.rows = M;
   q.K = w.K;
   cudaError_t e = launch_pdl(w4_prepare_kernel, (unsigned)M, kG4PrepThreads, q, st);
   if (e != cudaSuccess) return e;
@@ -1206,7 +1221,7 @@ size_t w4_experts_workspace_bytes(int64_t T, int64_t topk, const ql_w4_weight& w
   if (T <= kW4StreamMaxExpertTokens) return 0;
   const int64_t pairs = T * topk;
   const G4Plan g = plan_experts_host(pairs, w);
-  return g4_layout(combine ? pairs : T, w.K, pairs, g.tok_tiles, combine ? pairs * w.N : 0).total;
+  return g4_layout(pairs, w.K, pairs, g.tok_tiles, combine ? pairs * w.N : 0).total;
 }
 
 cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float* weights, const ql_w4_weight& w,
@@ -1214,27 +1229,34 @@ cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float
                               cudaStream_t st) {
   if (T <= kW4StreamMaxExpertTokens) return launch_w4_stream_experts(x, ids, weights, w, T, topk, y, st);
   const bool combine = weights != nullptr;
-  const int64_t pairs = T * topk, rows = combine ? pairs : T;
+  const int64_t pairs = T * topk;
   const G4Plan g = plan_experts_host(pairs, w);
-  const G4Layout L = g4_layout(rows, w.K, pairs, g.tok_tiles, combine ? pairs * w.N : 0);
+  const G4Layout L = g4_layout(pairs, w.K, pairs, g.tok_tiles, combine ? pairs * w.N : 0);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   G4PrepParams q = {};
   q.x = x;
   q.x16 = reinterpret_cast<uint16_t*>(ws + L.x16);
   q.ex = reinterpret_cast<int*>(ws + L.ex);
-  q.rows = rows;
   q.K = w.K;
   q.ids = ids;
   q.pairs = pairs;
   q.E = (int)w.experts;
   q.ntok = g.ntok;
-  q.topk = (int)topk;
+  q.slots = combine ? 1 : (int)topk;
   q.order = reinterpret_cast<int*>(ws + L.order);
   q.tiles = reinterpret_cast<G4Tile*>(ws + L.tiles);
   q.ntiles = reinterpret_cast<int*>(ws + L.ntiles);
   q.zero_y = combine ? nullptr : y;
   q.N = w.N;
-  cudaError_t e = launch_pdl(w4_prepare_experts_kernel, (unsigned)std::min<int64_t>(rows + 1, 4 * sms), kG4PlanThreads, q, st);
+  cudaError_t e;
+  const unsigned rows = (unsigned)(combine ? pairs : T);
+  if (pairs > kG4CountPairs) {
+    q.pos = reinterpret_cast<int*>(ws + L.pos);
+    if ((e = launch_pdl(w4_plan_kernel, 1, kG4PlanThreads, q, st)) != cudaSuccess) return e;
+    e = launch_pdl(w4_prepare_experts_kernel, rows, 256, q, st);
+  } else {
+    e = launch_pdl(w4_prepare_experts_kernel, rows + 1, kG4PlanThreads, q, st);
+  }
   if (e != cudaSuccess) return e;
   uint16_t* yp = combine ? reinterpret_cast<uint16_t*>(ws + L.yp) : y;
   G4Params p = {};
@@ -1243,9 +1265,8 @@ cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float
   p.order = q.order;
   p.tiles = q.tiles;
   p.ntiles = q.ntiles;
-  p.rows_per_token = combine ? 1 : (int)topk;
   p.status = status;
-  e = launch_g4<true>(w, q.x16, rows, p, g, sms, st);
+  e = launch_g4<true>(w, q.x16, pairs, p, g, sms, st);
   if (e != cudaSuccess || !combine) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)T, (unsigned)std::min<int64_t>(div_up(w.N, 128), 64));
