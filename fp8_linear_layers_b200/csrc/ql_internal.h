@@ -122,9 +122,11 @@ cudaError_t launch_gemm_small(ql_scheme scheme, const uint16_t* x, const void* w
 
 // 4-bit weights: few tokens on mma.sync, one pass over the weights for each 16
 // (dense) or 8 (experts) tokens.
-cudaError_t launch_w4_stream(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint16_t* y, cudaStream_t st);
+cudaError_t launch_w4_stream(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint16_t* y, int sms,
+                             cudaStream_t st);
 cudaError_t launch_w4_stream_experts(const uint16_t* x, const int32_t* ids, const float* weights,
-                                     const ql_w4_weight& w, int64_t T, int64_t topk, uint16_t* y, cudaStream_t st);
+                                     const ql_w4_weight& w, int64_t T, int64_t topk, uint16_t* y, int sms,
+                                     cudaStream_t st);
 // The product and the experts' products for any number of tokens: the kernels above
 // for few, tcgen05 for many.  workspace: *_workspace_bytes bytes of scratch.
 size_t w4_workspace_bytes(int64_t M, const ql_w4_weight& w, int sms);

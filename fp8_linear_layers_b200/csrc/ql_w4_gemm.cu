@@ -1008,21 +1008,46 @@ __global__ void __launch_bounds__(kG4PlanThreads) w4_prepare_experts_kernel(cons
 }
 
 // y[t] = sum_j weights[t, j] yp[t, j], the pairs' products rounded to bf16 (half the
-// traffic of f32 between the two kernels; one more rounding of each term).
-__global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restrict__ yp, const int32_t* __restrict__ ids,
+// traffic of f32 between the two kernels; one more rounding of each term).  A thread
+// takes kVec neighbouring outputs; bound by the pairs' bytes.
+template <int kVec>
+__global__ void __launch_bounds__(256) w4_combine_kernel(const uint16_t* __restrict__ yp, const int32_t* __restrict__ ids,
                                                          const float* __restrict__ weights, int topk, int E, int64_t N,
-                                                         uint16_t* __restrict__ y) {
+                                                         int64_t T, uint16_t* __restrict__ y) {
   tc::grid_dependency_wait();
   tc::launch_dependents();
-  const int64_t t = blockIdx.x;
-  for (int64_t n = (int64_t)blockIdx.y * 128 + threadIdx.x; n < N; n += (int64_t)gridDim.y * 128) {
-    float sum = 0.0f;
-    for (int j = 0; j < topk; ++j) {
-      const int e = __ldg(ids + t * topk + j);
-      if (e < 0 || e >= E) continue;
-      sum = fmaf(__ldg(weights + t * topk + j), bf16_lo(yp[(t * topk + j) * N + n]), sum);
+  const int64_t per = N / kVec, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= T * per) return;
+  const int64_t t = at / per, n = (at - t * per) * kVec;
+  float sum[kVec];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) sum[i] = 0.0f;
+#pragma unroll 4
+  for (int j = 0; j < topk; ++j) {
+    const int e = __ldg(ids + t * topk + j);
+    if (e < 0 || e >= E) continue;
+    const float w = __ldg(weights + t * topk + j);
+    const uint16_t* src = yp + (t * topk + j) * N + n;
+    if constexpr (kVec == 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src);
+      const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum[2 * i] = fmaf(w, bf16_lo(q[i]), sum[2 * i]);
+        sum[2 * i + 1] = fmaf(w, bf16_hi(q[i]), sum[2 * i + 1]);
+      }
+    } else {
+      sum[0] = fmaf(w, bf16_lo(*src), sum[0]);
     }
-    y[t * N + n] = f32_to_bf16_rn(sum);
+  }
+  if constexpr (kVec == 8) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = (uint32_t)f32_to_bf16_rn(sum[2 * i]) | (uint32_t)f32_to_bf16_rn(sum[2 * i + 1]) << 16;
+    *reinterpret_cast<uint4*>(y + t * N + n) = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
+    y[t * N + n] = f32_to_bf16_rn(sum[0]);
   }
 }
 
@@ -1198,7 +1223,7 @@ size_t w4_workspace_bytes(int64_t M, const ql_w4_weight& w, int sms) {
 
 cudaError_t launch_w4(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint16_t* y, void* workspace, int sms,
                       DevStatus* status, cudaStream_t st) {
-  if (M <= kW4StreamMaxTokens) return launch_w4_stream(x, w, M, y, st);
+  if (M <= kW4StreamMaxTokens) return launch_w4_stream(x, w, M, y, sms, st);
   const G4Plan g = plan_dense(M, w, sms);
   const G4Layout L = g4_layout(M, w.K, 0, 0, 0);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1227,7 +1252,7 @@ size_t w4_experts_workspace_bytes(int64_t T, int64_t topk, const ql_w4_weight& w
 cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float* weights, const ql_w4_weight& w,
                               int64_t T, int64_t topk, uint16_t* y, void* workspace, int sms, DevStatus* status,
                               cudaStream_t st) {
-  if (T <= kW4StreamMaxExpertTokens) return launch_w4_stream_experts(x, ids, weights, w, T, topk, y, st);
+  if (T <= kW4StreamMaxExpertTokens) return launch_w4_stream_experts(x, ids, weights, w, T, topk, y, sms, st);
   const bool combine = weights != nullptr;
   const int64_t pairs = T * topk;
   const G4Plan g = plan_experts_host(pairs, w);
@@ -1269,15 +1294,18 @@ cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float
   e = launch_g4<true>(w, q.x16, pairs, p, g, sms, st);
   if (e != cudaSuccess || !combine) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)T, (unsigned)std::min<int64_t>(div_up(w.N, 128), 64));
-  cfg.blockDim = dim3(128);
+  const int64_t threads = w.N % 8 ? T * w.N : T * (w.N / 8);
+  if (div_up(threads, 256) >= (int64_t(1) << 31)) return cudaErrorNotSupported;
+  cfg.gridDim = dim3((unsigned)div_up(threads, 256));
+  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, w4_combine_kernel, (const uint16_t*)yp, ids, weights, (int)topk, (int)w.experts, w.N, y);
+  return cudaLaunchKernelEx(&cfg, w.N % 8 ? w4_combine_kernel<1> : w4_combine_kernel<8>, (const uint16_t*)yp, ids,
+                            weights, (int)topk, (int)w.experts, w.N, T, y);
 }
 
 }  // namespace ql
