@@ -616,11 +616,13 @@ extern "C" ql_status qlinear_gemm_small_noalloc(ql_scheme scheme, const uint16_t
 // ---------------------------------------------------------------------------
 namespace {
 
+constexpr int64_t kW4MaxK = int64_t(1) << 24;
+
 // The shape of a 4-bit matrix; the pointers are checked by check_w4_pointers.
 ql_status check_w4_shape(const ql_w4_weight* w) {
   if (!w || w->N <= 0 || w->K <= 0 || w->experts <= 0) return QL_ERR_INVALID_ARG;
   if (w->group != 32 && w->group != 64 && w->group != 128) return QL_ERR_UNSUPPORTED_SHAPE;
-  if (w->K % 32 || w->K >= kIndexLimit || w->N >= kIndexLimit || w->experts >= kIndexLimit ||
+  if (w->K % 32 || w->K > kW4MaxK || w->N >= kIndexLimit || w->experts >= kIndexLimit ||
       w->experts * w->N > kIndexLimit - 512)
     return QL_ERR_UNSUPPORTED_SHAPE;
   return QL_OK;

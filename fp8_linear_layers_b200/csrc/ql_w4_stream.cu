@@ -46,54 +46,73 @@ struct W4StreamParams {
   int topk, E;
 };
 
-// A chunk's operands: weight words of rows g and g + 8, and x of the lane's tokens,
-// which for 16 tokens comes only when the chunk is multiplied (held ahead, two chunks
-// of it do not fit the registers).
-template <int V, int NT, bool kZero>
+// Where a lane's operands lie: everything but the chunk.
+template <int RT>
+struct W4Lane {
+  const uint8_t* wq;      // the tile's first row
+  const uint16_t* sw;
+  const uint8_t* wz;
+  uint32_t woff[2 * RT];  // this lane's rows (g + 8 i), bytes from the tile's first row to its first word
+  uint32_t soff[2 * RT];  // and scales
+
+  // Rows past N repeat row N - 1: loaded, not stored.
+  QL_DEVINL void rows(const W4StreamParams& p, int64_t n0, int g, int lane_bytes) {
+#pragma unroll
+    for (int i = 0; i < 2 * RT; ++i) {
+      const uint32_t r = (uint32_t)min((int64_t)(g + 8 * i), p.N - 1 - n0);
+      woff[i] = r * (uint32_t)(p.K >> 1) + lane_bytes;
+      soff[i] = r * (uint32_t)p.groups;
+    }
+  }
+  QL_DEVINL void tile(const W4StreamParams& p, int64_t row0) {
+    wq = p.wq + row0 * (p.K >> 1);
+    sw = p.sw + row0 * p.groups;
+    wz = p.wz + row0 * p.groups;
+  }
+};
+
+// A chunk's operands: weight words of the lane's 2 RT rows, and x of its tokens (null: a
+// column without a token).  x of 16 tokens comes only when the chunk is multiplied:
+// two chunks of it do not fit the registers.
+template <int V, int RT, int NT, bool kZero>
 struct W4Unit {
   static constexpr int kLoads = 4 / V;
-  static constexpr int kHeld = NT == 1 ? 4 : 1;
-  uint32_t w0[4], w1[4];
-  uint4 x[kHeld];
-  uint32_t s0[kLoads], s1[kLoads], z0[kZero ? kLoads : 1], z1[kZero ? kLoads : 1];
+  static constexpr bool kHeld = NT == 1;
+  uint32_t w[2 * RT][4];
+  uint32_t s[2 * RT][kLoads], z[kZero ? 2 * RT : 1][kLoads];
+  uint4 x[kHeld ? 4 : 1];
 
   static QL_DEVINL uint4 load_x(const W4StreamParams& p, const uint16_t* xr, int c, int i, int j, int t) {
-    const int64_t k = (int64_t)c * kW4Chunk + i * 32 * V + t * 8 * V;
-    return k < p.K && xr ? __ldg(reinterpret_cast<const uint4*>(xr + k) + j) : make_uint4(0, 0, 0, 0);
+    const int k = c * kW4Chunk + i * 32 * V + t * 8 * V;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (xr && k < (int)p.K) v = __ldg(reinterpret_cast<const uint4*>(xr + k) + j);
+    return v;
   }
 
-  QL_DEVINL void load(const W4StreamParams& p, int64_t row0, int64_t row1, const uint16_t* const (&xr)[NT],
-                      int c, int t) {
-    const uint8_t* a = p.wq + row0 * (p.K >> 1);
-    const uint8_t* b = p.wq + row1 * (p.K >> 1);
+  QL_DEVINL void load(const W4StreamParams& p, const W4Lane<RT>& l, const uint16_t* const (&xr)[NT], int c, int t) {
+    const bool whole = (c + 1) * kW4Chunk <= (int)p.K;  // every chunk but, where K % 128, the last
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int64_t k = (int64_t)c * kW4Chunk + i * 32 * V + t * 8 * V;  // this lane's first input
+      const uint32_t at = (uint32_t)c * (kW4Chunk / 2) + i * 16 * V;
       const int gi = c * kLoads + i;
-      uint32_t u[V], v[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) u[j] = v[j] = 0;
-      s0[i] = s1[i] = 0;
-      if constexpr (kZero) z0[i] = z1[i] = 8;
-      if (gi < p.groups) {
-        s0[i] = __ldg(p.sw + row0 * p.groups + gi);
-        s1[i] = __ldg(p.sw + row1 * p.groups + gi);
-        if constexpr (kZero) {
-          z0[i] = __ldg(p.wz + row0 * p.groups + gi);
-          z1[i] = __ldg(p.wz + row1 * p.groups + gi);
+      for (int r = 0; r < 2 * RT; ++r) {
+        uint32_t u[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) u[j] = 0;
+        s[r][i] = 0;
+        if constexpr (kZero) z[r][i] = 8;
+        if (whole || c * kW4Chunk + i * 32 * V + t * 8 * V < (int)p.K) w4::load_words<V>(l.wq + l.woff[r] + at, u);
+        if (whole || gi < p.groups) {
+          s[r][i] = __ldg(l.sw + l.soff[r] + gi);
+          if constexpr (kZero) z[r][i] = __ldg(l.wz + l.soff[r] + gi);
         }
-      }
-      const bool in = k < p.K;
-      if (in) {
-        w4::load_words<V>(a + (k >> 1), u);
-        w4::load_words<V>(b + (k >> 1), v);
-      }
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        w0[i * V + j] = u[j];
-        w1[i * V + j] = v[j];
-        if constexpr (NT == 1) x[i * V + j] = load_x(p, xr[0], c, i, j, t);
+        for (int j = 0; j < V; ++j) w[r][i * V + j] = u[j];
       }
+      if constexpr (kHeld)
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[i * V + j] = load_x(p, xr[0], c, i, j, t);
     }
   }
 
@@ -101,56 +120,66 @@ struct W4Unit {
   // `cw`, the weights of the two columns this lane holds, a column without a pair
   // (use0, use1) left alone.
   template <bool kWeighted>
-  QL_DEVINL void accumulate(float (&acc)[NT][4], const W4StreamParams& p, const uint16_t* const (&xr)[NT], int c, int t,
-                            float2 cw = {}, bool use0 = true, bool use1 = true) const {
+  QL_DEVINL void accumulate(float (&acc)[RT][NT][4], const W4StreamParams& p, const uint16_t* const (&xr)[NT], int c,
+                            int t, float2 cw = {}, bool use0 = true, bool use1 = true) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      float d[NT][4];
+      float d[RT][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) d[n][r] = 0.0f;
-      const uint32_t zz0 = kZero ? 0x43004300u | z0[i] * 0x10001u : 0x43084308u;
-      const uint32_t zz1 = kZero ? 0x43004300u | z1[i] * 0x10001u : 0x43084308u;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) d[r][n][k] = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        uint32_t a[4], b[4];
-        uint4 xn[NT];
+        uint32_t xb[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          if constexpr (NT == 1)
-            xn[n] = x[i * V + j];
+          uint4 v;
+          if constexpr (kHeld)
+            v = x[i * V + j];
           else
-            xn[n] = load_x(p, xr[n], c, i, j, t);
+            v = load_x(p, xr[n], c, i, j, t);
+          xb[n][0] = __byte_perm(v.x, v.z, 0x5410);
+          xb[n][1] = __byte_perm(v.x, v.z, 0x7632);
+          xb[n][2] = __byte_perm(v.y, v.w, 0x5410);
+          xb[n][3] = __byte_perm(v.y, v.w, 0x7632);
         }
-        w4::codes_to_bf16(w0[i * V + j], zz0, a);
-        w4::codes_to_bf16(w1[i * V + j], zz1, b);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 xv = xn[n];
-          w4::mma_bf16_16816(d[n], a[0], b[0], a[1], b[1], __byte_perm(xv.x, xv.z, 0x5410),
-                             __byte_perm(xv.x, xv.z, 0x7632));
-          w4::mma_bf16_16816(d[n], a[2], b[2], a[3], b[3], __byte_perm(xv.y, xv.w, 0x5410),
-                             __byte_perm(xv.y, xv.w, 0x7632));
+        for (int r = 0; r < RT; ++r) {
+          uint32_t a[4], b[4];
+          w4::codes_to_bf16(w[2 * r][i * V + j], kZero ? 0x43004300u | z[2 * r][i] * 0x10001u : 0x43084308u, a);
+          w4::codes_to_bf16(w[2 * r + 1][i * V + j], kZero ? 0x43004300u | z[2 * r + 1][i] * 0x10001u : 0x43084308u, b);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            w4::mma_bf16_16816(d[r][n], a[0], b[0], a[1], b[1], xb[n][0], xb[n][1]);
+            w4::mma_bf16_16816(d[r][n], a[2], b[2], a[3], b[3], xb[n][2], xb[n][3]);
+          }
         }
       }
-      const float f0 = __uint_as_float(s0[i] << 16), f1 = __uint_as_float(s1[i] << 16);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if constexpr (kWeighted) {
-          if (use0) {
-            acc[n][0] = fmaf(d[n][0] * f0, cw.x, acc[n][0]);
-            acc[n][2] = fmaf(d[n][2] * f1, cw.x, acc[n][2]);
+      for (int r = 0; r < RT; ++r) {
+        const float f0 = __uint_as_float(s[2 * r][i] << 16), f1 = __uint_as_float(s[2 * r + 1][i] << 16);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float(&o)[4] = acc[r][n];
+          const float(&q)[4] = d[r][n];
+          if constexpr (kWeighted) {
+            if (use0) {
+              o[0] = fmaf(q[0] * f0, cw.x, o[0]);
+              o[2] = fmaf(q[2] * f1, cw.x, o[2]);
+            }
+            if (use1) {
+              o[1] = fmaf(q[1] * f0, cw.y, o[1]);
+              o[3] = fmaf(q[3] * f1, cw.y, o[3]);
+            }
+          } else {
+            o[0] = fmaf(q[0], f0, o[0]);
+            o[1] = fmaf(q[1], f0, o[1]);
+            o[2] = fmaf(q[2], f1, o[2]);
+            o[3] = fmaf(q[3], f1, o[3]);
           }
-          if (use1) {
-            acc[n][1] = fmaf(d[n][1] * f0, cw.y, acc[n][1]);
-            acc[n][3] = fmaf(d[n][3] * f1, cw.y, acc[n][3]);
-          }
-        } else {
-          acc[n][0] = fmaf(d[n][0], f0, acc[n][0]);
-          acc[n][1] = fmaf(d[n][1], f0, acc[n][1]);
-          acc[n][2] = fmaf(d[n][2], f1, acc[n][2]);
-          acc[n][3] = fmaf(d[n][3], f1, acc[n][3]);
         }
       }
     }
@@ -176,35 +205,38 @@ QL_DEVINL void run_units(int first, int step, int n, Load load, Multiply multipl
   }
 }
 
-template <int V, int NT, bool kZero, W4Mode kMode>
+template <int V, int RT, int NT, bool kZero, W4Mode kMode>
 __global__ void __launch_bounds__(512) w4_stream_kernel(const W4StreamParams p) {
-  extern __shared__ float red[];     // [warps][16 rows][8 NT columns]
+  extern __shared__ float red[];     // [warps][16 RT rows][8 NT columns]
   __shared__ int s_pair[kW4Tokens];  // gather: the columns' pairs
-  using Unit = W4Unit<V, NT, kZero>;
+  using Unit = W4Unit<V, RT, NT, kZero>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int64_t n0 = (int64_t)blockIdx.x * kW4Rows;
-  const int64_t r0 = min(n0 + g, p.N - 1), r1 = min(n0 + g + 8, p.N - 1);  // rows past N: loaded, not stored
-  constexpr int kCols = NT * kW4Tokens;
+  constexpr int kCols = NT * kW4Tokens, kRows = RT * kW4Rows;
+  const int64_t n0 = (int64_t)blockIdx.x * kRows;
+  W4Lane<RT> l;
+  l.rows(p, n0, g, t * 4 * V);
 
   if constexpr (kMode == kW4Dense) {
     // The warp's first weights to L2 while the previous kernel on the stream ends.  (L2
     // is where that kernel's own writes go, so weights it may still be writing are
     // read correctly below.)
-    const int64_t k = ((int64_t)warp * kW4Chunk + t * 32) >> 1;
-    if (k < p.K >> 1) {
-      w4::prefetch_l2(p.wq + r0 * (p.K >> 1) + k);
-      w4::prefetch_l2(p.wq + r1 * (p.K >> 1) + k);
+    l.tile(p, n0);
+    if (warp < p.nchunk && (warp + 1) * kW4Chunk <= (int)p.K) {
+#pragma unroll
+      for (int i = 0; i < 2 * RT; ++i) w4::prefetch_l2(l.wq + l.woff[i] + warp * (kW4Chunk / 2));
     }
   }
   tc::grid_dependency_wait();
   tc::launch_dependents();
 
-  float acc[NT][4];
+  float acc[RT][NT][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) acc[n][r] = 0.0f;
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[r][n][k] = 0.0f;
 
   if constexpr (kMode == kW4Dense) {
     const int m0 = blockIdx.y * kCols;
@@ -215,7 +247,7 @@ __global__ void __launch_bounds__(512) w4_stream_kernel(const W4StreamParams p) 
       xr[n] = m < p.M ? p.x + (int64_t)m * p.K : nullptr;
     }
     run_units<Unit>(
-        warp, warps, p.nchunk, [&](Unit& u, int c) { u.load(p, r0, r1, xr, c, t); },
+        warp, warps, p.nchunk, [&](Unit& u, int c) { u.load(p, l, xr, c, t); },
         [&](const Unit& u, int c) { u.template accumulate<false>(acc, p, xr, c, t); });
   } else {
     // the CTA's block of up to 8 tokens and their (token, slot) pairs
@@ -252,8 +284,9 @@ __global__ void __launch_bounds__(512) w4_stream_kernel(const W4StreamParams p) 
       mine = __shfl_sync(0xffffffffu, column, g);
       if (valid) {
         const uint16_t* xr[1] = {mine >= 0 ? p.x + (int64_t)(t0 + mine / p.topk) * p.K : nullptr};
+        l.tile(p, e * p.N + n0);
         run_units<Unit>(
-            warp, warps, p.nchunk, [&](Unit& u, int c) { u.load(p, e * p.N + r0, e * p.N + r1, xr, c, t); },
+            warp, warps, p.nchunk, [&](Unit& u, int c) { u.load(p, l, xr, c, t); },
             [&](const Unit& u, int c) { u.template accumulate<false>(acc, p, xr, c, t); });
       }
     } else {
@@ -299,10 +332,10 @@ __global__ void __launch_bounds__(512) w4_stream_kernel(const W4StreamParams p) 
           warp, warps, count * p.nchunk,
           [&](Unit& u, int q) {
             const int i = q / p.nchunk;
-            const int64_t row = (int64_t)s_entry[i] * p.N;
+            l.tile(p, s_entry[i] * p.N + n0);
             const int mine = s_slot[i][g];
             const uint16_t* xr[1] = {mine >= 0 ? p.x + (pair0 + mine) * p.K : nullptr};
-            u.load(p, row + r0, row + r1, xr, q - i * p.nchunk, t);
+            u.load(p, l, xr, q - i * p.nchunk, t);
           },
           [&](const Unit& u, int q) {
             const int i = q / p.nchunk;
@@ -315,14 +348,16 @@ __global__ void __launch_bounds__(512) w4_stream_kernel(const W4StreamParams p) 
   }
 
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float* base = red + warp * kW4Rows * kCols + n * kW4Tokens + 2 * t;
-    *reinterpret_cast<float2*>(base + g * kCols) = make_float2(acc[n][0], acc[n][1]);
-    *reinterpret_cast<float2*>(base + (g + 8) * kCols) = make_float2(acc[n][2], acc[n][3]);
-  }
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float* base = red + (warp * kRows + r * kW4Rows) * kCols + n * kW4Tokens + 2 * t;
+      *reinterpret_cast<float2*>(base + g * kCols) = make_float2(acc[r][n][0], acc[r][n][1]);
+      *reinterpret_cast<float2*>(base + (g + 8) * kCols) = make_float2(acc[r][n][2], acc[r][n][3]);
+    }
   __syncthreads();
-  for (int i = threadIdx.x; i < kW4Rows * kCols; i += blockDim.x) {
-    const int row = i % kW4Rows, col = i / kW4Rows;
+  for (int i = threadIdx.x; i < kRows * kCols; i += blockDim.x) {
+    const int row = i % kRows, col = i / kRows;
     int64_t out = -1;  // y row of this column
     if constexpr (kMode == kW4Dense) {
       if (blockIdx.y * kCols + col < p.M) out = (int64_t)blockIdx.y * kCols + col;
@@ -333,36 +368,36 @@ __global__ void __launch_bounds__(512) w4_stream_kernel(const W4StreamParams p) 
     }
     if (out < 0 || n0 + row >= p.N) continue;
     float sum = 0.0f;
-    for (int w = 0; w < warps; ++w) sum += red[(w * kW4Rows + row) * kCols + col];
+    for (int w = 0; w < warps; ++w) sum += red[(w * kRows + row) * kCols + col];
     p.y[out * p.N + n0 + row] = f32_to_bf16_rn(sum);
   }
 }
 
 // ---------------------------------------------------------------------------- host
 
-template <int V, int NT, bool kZero, W4Mode kMode>
+template <int V, int RT, int NT, bool kZero, W4Mode kMode>
 static cudaError_t launch_t(const W4StreamParams& p, dim3 grid, int warps, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(warps * 32);
-  cfg.dynamicSmemBytes = (size_t)warps * kW4Rows * NT * kW4Tokens * sizeof(float);
+  cfg.dynamicSmemBytes = (size_t)warps * RT * kW4Rows * NT * kW4Tokens * sizeof(float);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, w4_stream_kernel<V, NT, kZero, kMode>, p);
+  return cudaLaunchKernelEx(&cfg, w4_stream_kernel<V, RT, NT, kZero, kMode>, p);
 }
 
-template <int NT, W4Mode kMode>
+template <int RT, int NT, W4Mode kMode>
 static cudaError_t launch_group(const W4StreamParams& p, int group, dim3 grid, int warps, cudaStream_t st) {
   const bool z = p.wz != nullptr;
   if (group == 128)
-    return z ? launch_t<4, NT, true, kMode>(p, grid, warps, st) : launch_t<4, NT, false, kMode>(p, grid, warps, st);
+    return z ? launch_t<4, RT, NT, true, kMode>(p, grid, warps, st) : launch_t<4, RT, NT, false, kMode>(p, grid, warps, st);
   if (group == 64)
-    return z ? launch_t<2, NT, true, kMode>(p, grid, warps, st) : launch_t<2, NT, false, kMode>(p, grid, warps, st);
-  return z ? launch_t<1, NT, true, kMode>(p, grid, warps, st) : launch_t<1, NT, false, kMode>(p, grid, warps, st);
+    return z ? launch_t<2, RT, NT, true, kMode>(p, grid, warps, st) : launch_t<2, RT, NT, false, kMode>(p, grid, warps, st);
+  return z ? launch_t<1, RT, NT, true, kMode>(p, grid, warps, st) : launch_t<1, RT, NT, false, kMode>(p, grid, warps, st);
 }
 
 static W4StreamParams stream_params(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint16_t* y) {
@@ -380,21 +415,31 @@ static W4StreamParams stream_params(const uint16_t* x, const ql_w4_weight& w, in
   return p;
 }
 
-// Warps of a CTA: as many as fill the SMs' 24 to 32 warps with one round of CTAs, so that
-// a warp has as many units as the size allows and none waits for another round.
-static int stream_warps(int64_t ctas, int nunit, int sms, int least) {
+// Warps of a CTA: as many as fill the SMs' 16 (32-row tiles) or 20 (16-row tiles) warps
+// with one round of CTAs, so that a warp has as many units as the size allows and none
+// waits for another round.
+static int stream_warps(int64_t ctas, int nunit, int64_t fill, int least) {
   int w = 16;
-  while (w > least && (ctas * w > (int64_t)sms * 28 || w > nunit)) w /= 2;
+  while (w > least && (ctas * w > fill || w > nunit)) w /= 2;
   return w;
 }
 
 cudaError_t launch_w4_stream(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint16_t* y, int sms,
                              cudaStream_t st) {
   const W4StreamParams p = stream_params(x, w, M, y);
+  const unsigned blocks = (unsigned)(M <= kW4Tokens ? 1 : (M + 15) / 16);
   const int64_t tiles = (w.N + kW4Rows - 1) / kW4Rows;
-  const int warps = stream_warps(tiles, p.nchunk, sms, 4);
-  if (M <= kW4Tokens) return launch_group<1, kW4Dense>(p, (int)w.group, dim3((unsigned)tiles, 1), warps, st);
-  return launch_group<2, kW4Dense>(p, (int)w.group, dim3((unsigned)tiles, (unsigned)((M + 15) / 16)), warps, st);
+  if (tiles >= 3 * sms) {
+    const int64_t wide = (w.N + 2 * kW4Rows - 1) / (2 * kW4Rows);
+    const int warps = stream_warps(wide * blocks, p.nchunk, 16 * sms, 4);
+    const dim3 grid((unsigned)wide, blocks);
+    return M <= kW4Tokens ? launch_group<2, 1, kW4Dense>(p, (int)w.group, grid, warps, st)
+                          : launch_group<2, 2, kW4Dense>(p, (int)w.group, grid, warps, st);
+  }
+  const int warps = stream_warps(tiles * blocks, p.nchunk, 20 * sms, 4);
+  const dim3 grid((unsigned)tiles, blocks);
+  return M <= kW4Tokens ? launch_group<1, 1, kW4Dense>(p, (int)w.group, grid, warps, st)
+                        : launch_group<1, 2, kW4Dense>(p, (int)w.group, grid, warps, st);
 }
 
 cudaError_t launch_w4_stream_experts(const uint16_t* x, const int32_t* ids, const float* weights,
@@ -407,11 +452,16 @@ cudaError_t launch_w4_stream_experts(const uint16_t* x, const int32_t* ids, cons
   p.E = (int)w.experts;
   const int64_t tiles = (w.N + kW4Rows - 1) / kW4Rows;
   const unsigned blocks = (unsigned)((T + kW4Tokens - 1) / kW4Tokens);
-  if (weights) return launch_group<1, kW4Combine>(p, (int)w.group, dim3((unsigned)tiles, 1, blocks), 16, st);
+  if (weights) return launch_group<1, 1, kW4Combine>(p, (int)w.group, dim3((unsigned)tiles, 1, blocks), 16, st);
   const int64_t pairs = std::min<int64_t>(T, kW4Tokens) * topk;
   const int64_t busy = std::min<int64_t>(pairs, w.experts);  // CTAs of a tile that do not leave at once, at most
-  const int warps = stream_warps(tiles * busy, p.nchunk, sms, 4);
-  return launch_group<1, kW4Gather>(p, (int)w.group, dim3((unsigned)tiles, (unsigned)pairs, blocks), warps, st);
+  if (tiles * busy >= 3 * sms) {
+    const int64_t wide = (w.N + 2 * kW4Rows - 1) / (2 * kW4Rows);
+    const int warps = stream_warps(wide * busy, p.nchunk, 16 * sms, 4);
+    return launch_group<2, 1, kW4Gather>(p, (int)w.group, dim3((unsigned)wide, (unsigned)pairs, blocks), warps, st);
+  }
+  const int warps = stream_warps(tiles * busy, p.nchunk, 20 * sms, 4);
+  return launch_group<1, 1, kW4Gather>(p, (int)w.group, dim3((unsigned)tiles, (unsigned)pairs, blocks), warps, st);
 }
 
 }  // namespace ql

@@ -423,8 +423,8 @@ size_t qlinear_forward_workspace_bytes(ql_scheme scheme, int64_t M, int64_t N, i
  *   wz     device, zero points z in 0..15, one byte each, laid out like sw; or
  *          NULL: z = 8 everywhere
  *   group  32, 64 or 128 inputs; the last group of a row may be shorter
- * Host struct, read during the call only.  K % 32 == 0, N and K below 2^31,
- * experts * N below 2^31; experts is 1 for a dense layer. */
+ * Host struct, read during the call only.  K % 32 == 0, K at most 2^24,
+ * experts * N at most 2^31 - 512; experts is 1 for a dense layer. */
 typedef struct ql_w4_weight {
   const void* wq;
   const uint16_t* sw;
