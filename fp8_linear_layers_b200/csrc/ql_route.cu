@@ -6,18 +6,22 @@
 //   best groups leave;  ids = the k largest c, ties to the lower index;
 //   w_j = p[id_j], divided by their sum when renormalized, times a scale.
 //
-// The floor is the logits' bytes (T E of 2 or 4 bytes); the selection's
-// instructions are what bounds the kernel.  One warp takes one token and keeps
-// its logits in registers, E / 32 to a lane, as unsigned keys that sort like the
-// values (0 = not available); a round of the selection is one warp-wide integer
-// maximum and one minimum of the indices that hold it.
+// The floor is the logits' bytes (T E of 2 or 4 bytes); the selection's instructions are
+// what bounds the kernel.  One warp takes one token.  Lane i keeps the experts
+// [i VPL, (i + 1) VPL) in registers, as unsigned keys that sort like the values (0 = not
+// available), so that a row is read in 16-byte pieces, the lowest lane that holds a
+// maximum holds its lowest index, and a group of experts is a run of lanes: all groups'
+// values come from one local pass and a few shuffles.  A round of the selection is one
+// warp-wide integer maximum, a ballot, and a new local maximum for the lane that lost
+// its own.
 //
 // Order must not depend on rounding.  Without a bias the keys are the logits
 // themselves.  With one (or when two scores are summed for a group) the f32 values
-// carry an error, so neighbours in the selected order, and the last chosen against
-// the best left out, are compared with a bound on it; a token with a pair inside
-// the bound is selected again from f64 values.  That is about one token in a few
-// hundred, so the common path stays f32.
+// carry an error, for which there is a bound.  Where two neighbours in the order, or the
+// last chosen and the best left out, are closer than that, the candidates that can
+// matter (at most 32, one to a lane) get their f64 values and are ranked by those; where
+// groups are that close, or more than 32 candidates, the token is selected again from
+// f64 values throughout.
 #include "ql_internal.h"
 #include "ql_w4.cuh"
 
@@ -26,9 +30,15 @@ namespace ql {
 constexpr int kRouteWarps = 4;
 constexpr unsigned kFull = 0xffffffffu;
 
-// Bound on the relative error of an f32 score: expf and the division are within
-// a few ulp and a softmax sum of up to 1024 terms within 2^-20; 2^-18 covers both.
-constexpr float kScoreErr = 0x1p-18f;
+// Bounds on the relative error of an f32 score of at least 1e-37 (what is below is always
+// compared in f64).  Sigmoid: expf is within 2^-23, 1 + e rounds to 2^-24, the
+// approximate reciprocal is within 2^-23 and the product rounds to 2^-24.  Softmax: the
+// difference d of two logits rounds to |d| 2^-24, of which |d| <= 88 matters, expf and
+// two roundings add 2^-22, and the sum's terms are off by the mean of that |d| (at most
+// 8 for 1024 terms) and its 37 additions by 2^-24 each.
+constexpr float kSigmoidErr = 0x1p-20f;
+constexpr float kSoftmaxErr = 0x1p-16f;
+constexpr float kScoreFloor = 1e-37f;
 constexpr float kRoundErr = 0x1p-22f;
 
 struct RouteParams {
@@ -40,6 +50,7 @@ struct RouteParams {
   int E, k;
   int sigmoid;
   int G, top_groups, group_top, gsize;
+  int glanes;  // lanes of a group where groups are runs of 2^n lanes, else 0
   uint32_t gmagic;  // e / gsize == e * gmagic >> 20 for e, gsize <= 1024
   int renormalize;
   float scale;
@@ -75,6 +86,13 @@ QL_DEVINL float load_logit(const void* row, int e) {
 QL_DEVINL bool usable(float l) { return l > -__int_as_float(0x7f800000); }
 QL_DEVINL float finite(float l) { return fminf(l, 3.402823466e38f); }
 
+// For comparisons: see kSigmoidErr.
+QL_DEVINL float sigmoid_fast(float l) {
+  const float e = expf(-fabsf(l));
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return l >= 0.0f ? r : e * r;
+}
 QL_DEVINL float sigmoid(float l) {
   const float e = expf(-fabsf(l));
   return (l >= 0.0f ? 1.0f : e) / (1.0f + e);
@@ -180,153 +198,254 @@ __device__ __noinline__ void select_f64(const RouteParams& p, const void* row, f
   }
 }
 
+// A candidate's exact choice (f64).
+template <bool kBf16>
+QL_DEVINL double choice_f64(const RouteParams& p, const void* row, int e, float lmax, double sum) {
+  const double d = (double)finite(load_logit<kBf16>(row, e));
+  const double v = p.sigmoid ? sigmoid(d) : exp(d - (double)lmax) / sum;
+  return v + (double)__ldg(p.bias + e);
+}
+
 template <int VPL, bool kBf16>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
   extern __shared__ double route_smem[];  // kRouteWarps rows of E doubles (scores by group or f64)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float none = -__int_as_float(0x7f800000);
   tc::grid_dependency_wait();
   tc::launch_dependents();
   const int64_t tok = (int64_t)blockIdx.x * kRouteWarps + warp;
   if (tok >= p.T) return;
   const void* row = static_cast<const char*>(p.logits) + tok * p.E * (kBf16 ? 2 : 4);
 
-  // logits, their maximum and (softmax) the sum
+  // logits (this lane's VPL, in 16-byte pieces where the row is whole) and their maximum
   float l[VPL];
-  float mx = -__int_as_float(0x7f800000);
+  const bool whole = p.E == 32 * VPL && VPL >= 4;
+  if (whole) {
+    if constexpr (kBf16 && VPL >= 8) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 32 + lane;
-    l[i] = e < p.E ? load_logit<kBf16>(row, e) : -__int_as_float(0x7f800000);
-    if (usable(l[i])) mx = fmaxf(mx, l[i] = finite(l[i]));
+      for (int i = 0; i < VPL / 8; ++i) {
+        const uint4 v = __ldg(static_cast<const uint4*>(row) + lane * (VPL / 8) + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          l[8 * i + 2 * j] = bf16_lo(w[j]);
+          l[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+        }
+      }
+    } else if constexpr (kBf16 && VPL == 4) {
+      const uint2 v = __ldg(static_cast<const uint2*>(row) + lane);
+      l[0] = bf16_lo(v.x), l[1] = bf16_hi(v.x), l[2] = bf16_lo(v.y), l[3] = bf16_hi(v.y);
+    } else if constexpr (!kBf16 && VPL >= 4) {
+#pragma unroll
+      for (int i = 0; i < VPL / 4; ++i) {
+        const float4 v = __ldg(static_cast<const float4*>(row) + lane * (VPL / 4) + i);
+        l[4 * i] = v.x, l[4 * i + 1] = v.y, l[4 * i + 2] = v.z, l[4 * i + 3] = v.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane * VPL + i;
+      l[i] = e < p.E ? load_logit<kBf16>(row, e) : none;
+    }
   }
-  mx = warp_max(mx);
+  float mx = none;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (usable(l[i])) mx = fmaxf(mx, l[i] = finite(l[i]));
   const bool scores = p.bias || (p.G > 1 && p.group_top == 2);  // values beyond the logits are compared
   float sum = 1.0f;
   if (!p.sigmoid && (scores || !p.renormalize)) {
+    mx = warp_max(mx);
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (usable(l[i])) s += expf(l[i] - mx);
     sum = warp_sum(s);
   }
+  const float inv = 1.0f / sum;
+  const float err = p.sigmoid ? kSigmoidErr : kSoftmaxErr;
+  auto score = [&](float v) { return p.sigmoid ? sigmoid_fast(v) : expf(v - mx) * inv; };
 
   uint32_t key[VPL];
+  if (p.bias) {
+    float b[VPL];
+    if (whole) {
+      if constexpr (VPL >= 4)
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    key[i] = 0;
-    if (usable(l[i])) {
-      float v = l[i];
-      if (p.bias) {
-        const float b = __ldg(p.bias + i * 32 + lane);
-        v = (p.sigmoid ? sigmoid(v) : expf(v - mx) / sum) + b;
-        if (!usable(b)) v = __int_as_float(0x7fffffff);
-      }
-      if (v == v) key[i] = order_key(v);
+        for (int i = 0; i < VPL / 4; ++i) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(p.bias) + lane * (VPL / 4) + i);
+          b[4 * i] = v.x, b[4 * i + 1] = v.y, b[4 * i + 2] = v.z, b[4 * i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) b[i] = lane * VPL + i < p.E ? __ldg(p.bias + lane * VPL + i) : none;
     }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = usable(l[i]) && usable(b[i]) ? order_key(score(l[i]) + b[i]) : 0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = usable(l[i]) ? order_key(l[i]) : 0;
   }
 
   bool unsure = false;
   if (p.G > 1) {
-    float* c = reinterpret_cast<float*>(route_smem + warp * p.E);
-    const float none = -__int_as_float(0x7f800000);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * 32 + lane;
-      if (e < p.E) {
-        float v = none;
-        if (key[i])
-          v = p.bias || p.group_top == 1 ? key_value(key[i]) : p.sigmoid ? sigmoid(l[i]) : expf(l[i] - mx) / sum;
-        c[e] = v;
-      }
-    }
-    __syncwarp();
+    // every group's value and a bound on its error, on the lane of the group's number or
+    // (runs of lanes) on all of the group's lanes
     uint32_t gkey = 0;
     float gerr = 0.0f;
-    if (lane < p.G) {
-      float a = none, b = none;
-      int off = lane % p.gsize;  // rotated: the groups' rows start on different banks
-      for (int i = 0; i < p.gsize; ++i) {
-        const float v = c[lane * p.gsize + off];
-        off = off + 1 == p.gsize ? 0 : off + 1;
-        b = fmaxf(b, fminf(a, v));
-        a = fmaxf(a, v);
+    float a = none, b = none;  // the group's two largest
+    auto add = [&](float v) {
+      b = fmaxf(b, fminf(a, v));
+      a = fmaxf(a, v);
+    };
+    const bool by_key = p.bias || p.group_top == 1;
+    bool member;  // this lane stands for a group
+    if (p.glanes) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) add(!key[i] ? none : by_key ? key_value(key[i]) : score(l[i]));
+      for (int o = 1; o < p.glanes; o <<= 1) {
+        const float oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
+        add(oa);
+        add(ob);
       }
+      member = lane < p.G * p.glanes;
+    } else {
+      float* c = reinterpret_cast<float*>(route_smem + warp * p.E);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (lane * VPL + i < p.E) c[lane * VPL + i] = !key[i] ? none : by_key ? key_value(key[i]) : score(l[i]);
+      __syncwarp();
+      member = lane < p.G;
+      if (member) {
+        int off = lane % p.gsize;  // rotated: the groups' rows start on different banks
+        for (int i = 0; i < p.gsize; ++i) {
+          add(c[lane * p.gsize + off]);
+          off = off + 1 == p.gsize ? 0 : off + 1;
+        }
+      }
+      __syncwarp();
+    }
+    if (member) {
       const float gs = p.group_top == 1 ? a : a + b;
       gkey = order_key(gs);
-      gerr = usable(gs) ? 2.0f * kScoreErr + kRoundErr * (fabsf(a) + fabsf(b)) : 0.0f;
-      if (p.group_top == 1) gerr = p.bias ? kScoreErr + kRoundErr * fabsf(a) : 0.0f;
-      if (!usable(gs)) gerr = 0.0f;
+      // scores are at most 1; without a bias a single largest is a logit, and exact
+      if (scores && usable(gs))
+        gerr = p.group_top == 1 ? err + kRoundErr * fabsf(a) : 2.0f * err + kRoundErr * (fabsf(a) + fabsf(b));
     }
-    __syncwarp();
-    uint32_t kept = 0;
-    float low = 0.0f;  // the smallest value kept, less its error
+    uint32_t kept = 0;  // by group
+    float low = 0.0f;   // the smallest value kept, less its error
     for (int r = 0; r < p.top_groups; ++r) {
       const uint32_t m = __reduce_max_sync(kFull, gkey);
       const int win = __ffs(__ballot_sync(kFull, gkey == m)) - 1;
-      kept |= 1u << win;
+      const int group = p.glanes ? win / p.glanes : win;
+      kept |= 1u << group;
       const float v = key_value(m) - __shfl_sync(kFull, gerr, win);
       low = r == 0 ? v : fminf(low, v);
-      if (lane == win) gkey = 0;
+      if ((p.glanes ? lane / p.glanes : lane) == group) gkey = 0;
     }
-    if (scores) {
-      const bool close = gkey && gerr > 0.0f && key_value(gkey) + gerr >= low;
-      unsure = __any_sync(kFull, close);
-    }
+    if (scores) unsure = __any_sync(kFull, gkey && gerr > 0.0f && key_value(gkey) + gerr >= low);
+    if (p.glanes) {
+      if (!((kept >> (lane / p.glanes & 31)) & 1u)) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (!((kept >> ((((i * 32 + lane) * p.gmagic) >> 20) & 31)) & 1u)) key[i] = 0;
+        for (int i = 0; i < VPL; ++i) key[i] = 0;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (!((kept >> ((((lane * VPL + i) * p.gmagic) >> 20) & 31)) & 1u)) key[i] = 0;
+    }
   }
 
-  // k rounds (one more where the choice may have to be confirmed); lane j keeps round j's winner
+  // k rounds; lane j keeps round j's winner
   uint32_t best = 0;
   int best_i = 0;
+  auto local_best = [&] {
+    best = 0;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (key[i] > best) {
-      best = key[i];
-      best_i = i;
-    }
+    for (int i = 0; i < VPL; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        best_i = i;
+      }
+  };
+  local_best();
   int my_id = -1;
-  uint32_t my_key = 0, next_key = 0;
-  for (int j = 0; j < p.k; ++j) {
+  uint32_t my_key = 0;
+  auto round = [&](int j) {  // false: none left
     const uint32_t m = __reduce_max_sync(kFull, best);
-    if (m == 0) break;
-    const int win = (int)__reduce_min_sync(kFull, best == m ? (unsigned)(best_i * 32 + lane) : kFull);
+    if (m == 0) return false;
+    const int win = __ffs(__ballot_sync(kFull, best == m)) - 1;  // the lowest lane has the lowest index
+    const int id = win * VPL + __shfl_sync(kFull, best_i, win);
     if (lane == j) {
-      my_id = win;
+      my_id = id;
       my_key = m;
     }
-    if ((win & 31) == lane) {
-      best = 0;
+    if (lane == win) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (i == (win >> 5)) key[i] = 0;
-        if (key[i] > best) {
-          best = key[i];
-          best_i = i;
-        }
-      }
+      for (int i = 0; i < VPL; ++i)
+        if (i == best_i) key[i] = 0;
+      local_best();
     }
-  }
+    return true;
+  };
+  int n = 0;
+  while (n < p.k && round(n)) ++n;
   if (p.bias && !unsure) {
     // neighbours in the order whose f32 distance does not settle it
     const uint32_t left = __reduce_max_sync(kFull, best);
-    next_key = __shfl_down_sync(kFull, my_key, 1);
-    if (lane == p.k - 1) next_key = left;
     float mine = 0.0f, b = 0.0f;
     if (my_id >= 0) {
       mine = load_logit<kBf16>(row, my_id);
       b = __ldg(p.bias + my_id);
     }
+    uint32_t next = __shfl_down_sync(kFull, my_key, 1);
     const float next_l = __shfl_down_sync(kFull, mine, 1), next_b = __shfl_down_sync(kFull, b, 1);
+    const bool border = lane == p.k - 1;
+    if (border) next = left;
     bool close = false;
-    if (my_id >= 0 && next_key) {
-      const float c0 = key_value(my_key), c1 = key_value(next_key);
-      const bool same = lane < p.k - 1 && mine == next_l && b == next_b;
-      const float nb = lane < p.k - 1 ? fabsf(next_b) : fabsf(c1) + 1.0f;
-      close = !same && !(c0 - c1 > kScoreErr * (fabsf(c0) + fabsf(b) + fabsf(c1) + nb));
+    const float c0 = key_value(my_key);
+    if (my_id >= 0 && next) {
+      const float c1 = key_value(next);
+      const bool same = !border && mine == next_l && b == next_b;
+      const float nb = border ? fabsf(c1) + 1.0f : fabsf(next_b);
+      close = !same && !(c0 - c1 > err * (fabsf(c0) + fabsf(b) + fabsf(c1) + nb) + kScoreFloor);
     }
-    unsure = __any_sync(kFull, close);
+    if (__any_sync(kFull, close)) {
+      // more candidates, while they may reach the last chosen one; then all by their f64 values
+      const uint32_t kth = __shfl_sync(kFull, my_key, p.k - 1);
+      bool more = kth != 0;
+      const float cut = key_value(kth) - 2.0f * err * (2.0f * fabsf(key_value(kth)) + 2.0f) - kScoreFloor;
+      while (n < 32 && more) {
+        const uint32_t m = __reduce_max_sync(kFull, best);
+        more = m != 0 && !(key_value(m) < cut);
+        if (more && round(n)) ++n;
+      }
+      unsure = more;
+      if (!unsure) {
+        double total = 1.0;
+        if (!p.sigmoid) {
+          double s = 0.0;
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (usable(l[i])) s += exp((double)l[i] - (double)mx);
+          total = warp_sum(s);
+        }
+        const double c = my_id >= 0 ? choice_f64<kBf16>(p, row, my_id, mx, total) : 0.0;
+        int rank = 0;
+        for (int i = 0; i < n; ++i) {
+          const double oc = __shfl_sync(kFull, c, i);
+          const int oid = __shfl_sync(kFull, my_id, i);
+          rank += oc > c || (oc == c && oid < my_id);
+        }
+        int out = -1;
+        for (int i = 0; i < n; ++i) {
+          const int orank = __shfl_sync(kFull, rank, i), oid = __shfl_sync(kFull, my_id, i);
+          if (orank == lane) out = oid;
+        }
+        my_id = lane < p.k ? out : -1;
+      }
+    }
   }
   if (unsure) select_f64<VPL, kBf16>(p, row, mx, route_smem + warp * p.E, lane, my_id);
 
@@ -336,7 +455,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
   float w = 0.0f;
   if (p.renormalize) {
     // scaled by a common factor so that the largest is near 1: w_j / sum does not underflow
-    const float top = warp_max(has ? (p.sigmoid ? fminf(lj, 0.0f) : lj) : -__int_as_float(0x7f800000));
+    const float top = warp_max(has ? (p.sigmoid ? fminf(lj, 0.0f) : lj) : none);
     if (has) w = p.sigmoid ? expf(fminf(lj, 0.0f) - top) / (1.0f + expf(-fabsf(lj))) : expf(lj - top);
     const float s = warp_sum(w);
     if (has) w = w / s;
@@ -394,6 +513,8 @@ cudaError_t launch_route(const void* logits, bool bf16, const ql_route_config& c
   p.top_groups = (int)c.top_groups;
   p.group_top = (int)c.group_top;
   p.gsize = p.E / p.G;
+  const int vpl = p.E <= 32 ? 1 : p.E <= 64 ? 2 : p.E <= 128 ? 4 : p.E <= 256 ? 8 : p.E <= 512 ? 16 : 32;
+  if (p.gsize % vpl == 0 && ((p.gsize / vpl) & (p.gsize / vpl - 1)) == 0) p.glanes = p.gsize / vpl;
   p.gmagic = (uint32_t)(((1u << 20) + p.gsize - 1) / p.gsize);
   p.renormalize = c.renormalize != 0;
   p.scale = c.scale;
