@@ -672,9 +672,9 @@ def route(logits: torch.Tensor, top_k: int, score: int = ROUTE_SOFTMAX, bias: to
         if bias.numel() != E:
             raise ValueError(f"bias must have {E} entries")
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        ids = logits.new_empty((T, top_k), dtype=torch.int32)
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+        weights = logits.new_empty((T, top_k), dtype=torch.float32)
     if tuple(ids.shape) != (T, top_k) or tuple(weights.shape) != (T, top_k):
         raise ValueError(f"ids and weights must be {(T, top_k)}")
     c = _route_config(E, top_k, groups, top_groups, group_top, score, bool(renormalize), scale)

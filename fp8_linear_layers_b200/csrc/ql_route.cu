@@ -370,18 +370,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
       }
   };
   local_best();
-  int my_id = -1;
-  uint32_t my_key = 0;
+  __shared__ uint2 s_won[kRouteWarps][32];  // the rounds' winners: key, expert
   auto round = [&](int j) {  // false: none left
     const uint32_t m = __reduce_max_sync(kFull, best);
     if (m == 0) return false;
-    const int win = __ffs(__ballot_sync(kFull, best == m)) - 1;  // the lowest lane has the lowest index
-    const int id = win * VPL + __shfl_sync(kFull, best_i, win);
-    if (lane == j) {
-      my_id = id;
-      my_key = m;
-    }
-    if (lane == win) {
+    const unsigned at = __ballot_sync(kFull, best == m);
+    if (best == m && (at & ((1u << lane) - 1u)) == 0) {  // the lowest lane has the lowest index
+      s_won[warp][j] = make_uint2(m, (unsigned)(lane * VPL + best_i));
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
         if (i == best_i) key[i] = 0;
@@ -390,7 +385,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
     return true;
   };
   int n = 0;
+#pragma unroll 1
   while (n < p.k && round(n)) ++n;
+  int my_id = -1;
+  uint32_t my_key = 0;
+  auto collect = [&] {  // lane j takes round j's winner
+    __syncwarp();
+    if (lane < n) {
+      my_key = s_won[warp][lane].x;
+      my_id = (int)s_won[warp][lane].y;
+    }
+  };
+  collect();
   if (p.bias && !unsure) {
     // neighbours in the order whose f32 distance does not settle it
     const uint32_t left = __reduce_max_sync(kFull, best);
@@ -421,6 +427,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
         more = m != 0 && !(key_value(m) < cut);
         if (more && round(n)) ++n;
       }
+      collect();
       unsure = more;
       if (!unsure) {
         double total = 1.0;
@@ -447,17 +454,23 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
       }
     }
   }
-  if (unsure) select_f64<VPL, kBf16>(p, row, mx, route_smem + warp * p.E, lane, my_id);
+  if (unsure) {
+    select_f64<VPL, kBf16>(p, row, mx, route_smem + warp * p.E, lane, my_id);
+    if (!p.bias && my_id >= 0) my_key = order_key(finite(load_logit<kBf16>(row, my_id)));
+  }
 
   // weights of the chosen experts, one to a lane
   const bool has = lane < p.k && my_id >= 0;
-  const float lj = has ? finite(load_logit<kBf16>(row, my_id)) : 0.0f;
+  float lj = 0.0f;  // without a bias the key is the logit
+  if (has) lj = p.bias ? finite(load_logit<kBf16>(row, my_id)) : key_value(my_key);
   float w = 0.0f;
   if (p.renormalize) {
     // scaled by a common factor so that the largest is near 1: w_j / sum does not underflow
-    const float top = warp_max(has ? (p.sigmoid ? fminf(lj, 0.0f) : lj) : none);
+    float top = p.sigmoid ? fminf(lj, 0.0f) : lj;
+    top = p.bias ? warp_max(has ? top : none) : __shfl_sync(kFull, top, 0);
     if (has) w = p.sigmoid ? expf(fminf(lj, 0.0f) - top) / (1.0f + expf(-fabsf(lj))) : expf(lj - top);
-    const float s = warp_sum(w);
+    float s = w;
+    for (int o = 1; o < p.k; o <<= 1) s += __shfl_xor_sync(kFull, s, o);
     if (has) w = w / s;
   } else if (has) {
     w = p.sigmoid ? sigmoid(lj) : expf(lj - mx) / sum;
