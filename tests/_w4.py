@@ -23,6 +23,11 @@ def dequantize(wq, sw, wz, group):
     return (q - z).double() * sw[..., k // group].double()
 
 
+def magnitudes(wq, sw, wz, group):
+    """[..., K] float64: |q - z| |s|, the size of a weight."""
+    return dequantize(wq, sw, wz, group).abs()
+
+
 def product_limit(y, mag, K, zeros=False):
     """Largest allowed |kernel - exact|: the output's bf16 rounding (half a step:
     2^-8 of the value), and f32 sums of exact products: K / 16 tensor-core steps
@@ -38,12 +43,13 @@ def product_limit(y, mag, K, zeros=False):
     return 2.0 ** -8 * y.abs() + ((K / 16 + 64) * 2.0 ** -22 + (2.0 ** -11 if zeros else 0.0)) * mag + 1e-38
 
 
-def assert_product(got, x, w, zeros=False, what=""):
-    """got bf16 [M,N] against x [M,K] @ w[N,K]^T in float64."""
+def assert_product(got, x, wq, sw, wz, group, what=""):
+    """got bf16 [M,N] against x [M,K] @ W[N,K]^T in float64."""
+    w = dequantize(wq, sw, wz, group)
     y = x.double() @ w.t()
-    mag = x.double().abs() @ w.abs().t()
+    mag = x.double().abs() @ magnitudes(wq, sw, wz, group).t()
     err = (got.double().cpu() - y).abs()
-    lim = product_limit(y, mag, w.shape[1], zeros)
+    lim = product_limit(y, mag, w.shape[1], wz is not None)
     bad = (~(err <= lim)).nonzero()
     assert bad.numel() == 0, (what, bad.shape[0], [(tuple(b.tolist()), got.double().cpu()[tuple(b)].item(),
                                                     y[tuple(b)].item(), lim[tuple(b)].item()) for b in bad[:4]])
@@ -99,8 +105,9 @@ def route64(logits, k, sigmoid=False, bias=None, groups=1, top_groups=1, group_t
     return ids, wts
 
 
-def experts64(x, ids, w, weights=None):
-    """x [T,K] (gather) or [T,k,K] (combine), w [E,N,K] float64 -> (value, magnitude)."""
+def experts64(x, ids, w, size, weights=None):
+    """x [T,K] (gather) or [T,k,K] (combine), w [E,N,K] float64 and size its magnitudes ->
+    (value, magnitude)."""
     T, k = ids.shape
     E, N, _ = w.shape
     shape = (T, N) if weights is not None else (T, k, N)
@@ -111,7 +118,7 @@ def experts64(x, ids, w, weights=None):
             if not 0 <= e < E:
                 continue
             row = (x[t, j] if weights is not None else x[t]).double()
-            v, m = w[e] @ row, w[e].abs() @ row.abs()
+            v, m = w[e] @ row, size[e] @ row.abs()
             if weights is None:
                 y[t, j], mag[t, j] = v, m
             else:

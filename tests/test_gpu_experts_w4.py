@@ -36,13 +36,13 @@ def _check(x, ids, wq, sw, wz, wts, group):
     ql.experts_w4(x.cuda(), ids.cuda(), w, weights=wts.cuda() if combine else None, y=y)
     assert ql.device_status()[0] == 0
     assert buf[:256].isnan().all() and buf[256 + n:].isnan().all()
-    ref, mag = _w4.experts64(x, ids, _w4.dequantize(wq, sw, wz, group), wts)
+    wd, size = _w4.dequantize(wq, sw, wz, group), _w4.magnitudes(wq, sw, wz, group)
+    ref, mag = _w4.experts64(x, ids, wd, size, wts)
     lim = _w4.product_limit(ref, mag, x.shape[-1], wz is not None)
     if combine:
         # sum_j |w_j| |y_j| <= the magnitude, but a bf16 rounding is relative to each
         # pair's own value: bound it by the pairs' values
-        wd = _w4.dequantize(wq, sw, wz, group)
-        pairs, _ = _w4.experts64(x.reshape(T * k, -1), ids.reshape(T * k, 1), wd)
+        pairs, _ = _w4.experts64(x.reshape(T * k, -1), ids.reshape(T * k, 1), wd, size)
         lim = lim + 2.0 ** -8 * (pairs.view(T, k, N).abs() * wts.double().abs()[..., None]).sum(1)
     err = (y.double().cpu() - ref).abs()
     assert (err <= lim).all(), (err - lim).max()
@@ -58,7 +58,16 @@ def test_experts(cuda, combine, group, zeros, T, k, E, N, K):
 
 
 @pytest.mark.parametrize("combine", [False, True])
-@pytest.mark.parametrize("T", [1, 5, 8, 40])
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True)])
+@pytest.mark.parametrize("T", [2, 7, 9, 16, 17])
+def test_large_experts_for_few_tokens(cuda, combine, group, zeros, T):
+    x, ids, wq, sw, wz, wts = _case(T, 4, 6, 2056, 1056, group, zeros, combine)
+    ids[0, 1], ids[-1, 2] = ids[0, 0], -1  # an expert twice, and none
+    _check(x, ids, wq, sw, wz, wts, group)
+
+
+@pytest.mark.parametrize("combine", [False, True])
+@pytest.mark.parametrize("T", [1, 5, 8, 13, 40])
 @pytest.mark.parametrize("kind", ["one expert", "same expert twice", "out of range", "nothing"])
 def test_uneven_ids(cuda, combine, T, kind):
     x, ids, wq, sw, wz, wts = _case(T, 4, 6, 40, 128, 64, False, combine)
@@ -135,11 +144,11 @@ def test_route_up_activation_down(cuda, T):
         ids, wts, h, act, y = (o.cpu() for o in out)
         rid, _ = _w4.route64(logits, k, True, None, groups=4, top_groups=2, group_top=2, scale=2.0)
         assert (ids.numpy() == rid).all()
-        wu, wd = _w4.dequantize(*up_h, 64), _w4.dequantize(*down_h, 32)
-        ref, mag = _w4.experts64(x, ids, wu)
+        ref, mag = _w4.experts64(x, ids, _w4.dequantize(*up_h, 64), _w4.magnitudes(*up_h, 64))
         assert ((h.double() - ref).abs() <= _w4.product_limit(ref, mag, H)).all()
-        ref, mag = _w4.experts64(act, ids, wd, wts)
-        pairs, _ = _w4.experts64(act.reshape(T * k, I), ids.reshape(T * k, 1), wd)
+        wd, size = _w4.dequantize(*down_h, 32), _w4.magnitudes(*down_h, 32)
+        ref, mag = _w4.experts64(act, ids, wd, size, wts)
+        pairs, _ = _w4.experts64(act.reshape(T * k, I), ids.reshape(T * k, 1), wd, size)
         lim = _w4.product_limit(ref, mag, I, True) + 2.0 ** -8 * (pairs.view(T, k, H).abs() * wts.double()[..., None]).sum(1)
         assert ((y.double() - ref).abs() <= lim).all()
 

@@ -37,7 +37,7 @@ def _check(x, wq, sw, wz, group, what=""):
     out = ql.forward_w4(x.cuda(), _handle(wq, sw, wz, group), y=y)
     assert out is y and ql.device_status()[0] == 0
     assert buf[:256].isnan().all() and buf[256 + M * N:].isnan().all()
-    _w4.assert_product(y, x, _w4.dequantize(wq, sw, wz, group), wz is not None, what)
+    _w4.assert_product(y, x, wq, sw, wz, group, what)
     return y
 
 
@@ -50,11 +50,13 @@ def test_product(cuda, group, zeros, M, N, K):
     _check(*_case(M, N, K, group, zeros), group)
 
 
-@pytest.mark.parametrize("M,N,K,group", [(1, 1024, 4096, 128), (3, 4096, 14336, 128), (12, 14336, 4096, 64),
-                                         (24, 4096, 4096, 32), (512, 1024, 4096, 128)])
-def test_product_layer_sizes(cuda, M, N, K, group):
+@pytest.mark.parametrize("M,N,K,group,zeros", [
+    (1, 1024, 4096, 128, False), (3, 4096, 14336, 128, True), (12, 14336, 4096, 64, False), (24, 4096, 4096, 32, True),
+    (512, 1024, 4096, 128, False), (1, 4096, 4096, 32, True), (8, 6144, 4096, 64, True), (16, 4096, 4160, 128, True),
+    (2, 5003, 4128, 128, False), (9, 14336, 992, 32, False)])
+def test_product_layer_sizes(cuda, M, N, K, group, zeros):
     """Decoder layer sizes, and the same call twice in one workspace gives the same bits."""
-    x, wq, sw, wz = _case(M, N, K, group, False)
+    x, wq, sw, wz = _case(M, N, K, group, zeros)
     y = _check(x, wq, sw, wz, group)
     w = _handle(wq, sw, wz, group)
     ws = ql.new_workspace(ql.forward_w4_workspace_bytes(M, w))
@@ -69,11 +71,11 @@ def test_no_tokens(cuda):
     assert y.shape == (0, 64)
 
 
-@pytest.mark.parametrize("M", [1, 12, 40])
-def test_wide_range(cuda, M):
+@pytest.mark.parametrize("M,N,K", [(1, 70, 512), (12, 70, 512), (40, 70, 512), (3, 4096, 4096), (16, 4096, 4096)])
+def test_wide_range(cuda, M, N, K):
     """Scales 2^-100 .. 2^20 in one row, tokens 2^-60 .. 2^60 apart: nothing is lost
     to the operands' range."""
-    N, K, group = 70, 512, 64
+    group = 64
     g = _gen(3)
     x, wq, sw, _ = _case(M, N, K, group, False, seed=3)
     x = (x.float() * 2.0 ** torch.randint(-60, 60, (M, 1), generator=g)).bfloat16()
@@ -92,9 +94,9 @@ def test_zero_scales_and_tokens(cuda, M):
     assert not y[M // 2].any() and not y[:, 5].any()
 
 
-@pytest.mark.parametrize("M", [1, 9, 40])
-def test_infinite_and_nan_tokens_stay_in_their_row(cuda, M):
-    x, wq, sw, wz = _case(M + 2, 80, 256, 128, False)
+@pytest.mark.parametrize("M,N,K", [(1, 80, 256), (9, 80, 256), (40, 80, 256), (4, 4096, 4096)])
+def test_infinite_and_nan_tokens_stay_in_their_row(cuda, M, N, K):
+    x, wq, sw, wz = _case(M + 2, N, K, 128, False)
     clean = ql.forward_w4(x.cuda(), _handle(wq, sw, wz, 128))
     x[0, 7] = float("inf")
     x[1, 9] = float("nan")
@@ -113,11 +115,11 @@ def test_row_results_do_not_depend_on_the_batch(cuda):
     assert torch.equal(ql.forward_w4(x[:1].cuda(), w), full[:1])
 
 
-@pytest.mark.parametrize("M", [1, 16, 50])
-def test_side_stream_and_graph(cuda, M):
+@pytest.mark.parametrize("M,N,K", [(1, 144, 384), (16, 144, 384), (50, 144, 384), (5, 4096, 4096), (300, 520, 384)])
+def test_side_stream_and_graph(cuda, M, N, K):
     """On another stream than the current one, and captured: the replay reads the
     inputs, the weights and the zero points as they are then."""
-    x, wq, sw, wz = _case(M, 144, 384, 64, True)
+    x, wq, sw, wz = _case(M, N, K, 64, True)
     xd, w = x.cuda(), _handle(wq, sw, wz, 64)
     ref = ql.forward_w4(xd, w)
     side = torch.cuda.Stream()
@@ -130,19 +132,19 @@ def test_side_stream_and_graph(cuda, M):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         ql.forward_w4(xd, w, workspace=ws, y=out)
-    x2, wq2, sw2, wz2 = _case(M, 144, 384, 64, True, seed=9)
+    x2, wq2, sw2, wz2 = _case(M, N, K, 64, True, seed=9)
     for d, h in ((xd, x2), (w.wq, wq2), (w.sw, sw2), (w.wz, wz2)):
         d.copy_(h)
     graph.replay()
     torch.cuda.synchronize()
-    _w4.assert_product(out, x2, _w4.dequantize(wq2, sw2, wz2, 64), True)
+    _w4.assert_product(out, x2, wq2, sw2, wz2, 64)
 
 
-@pytest.mark.parametrize("M", [1, 40])
-def test_weights_written_just_before_on_the_stream(cuda, M):
+@pytest.mark.parametrize("M,N,K", [(1, 512, 2048), (40, 512, 2048), (2, 4096, 4096), (200, 512, 2048)])
+def test_weights_written_just_before_on_the_stream(cuda, M, N, K):
     """The weights may come from work still in flight on the same stream."""
-    x, wq, sw, wz = _case(M, 512, 2048, 128, False)
-    w0 = torch.randn(512, 2048, generator=_gen(5)).bfloat16().cuda()
+    x, wq, sw, wz = _case(M, N, K, 128, False)
+    w0 = torch.randn(N, K, generator=_gen(5)).bfloat16().cuda()
     xd = x.cuda()
     ref = ql.forward_w4(xd, ql.quantize_weight_w4(w0))
     torch.cuda.synchronize()
