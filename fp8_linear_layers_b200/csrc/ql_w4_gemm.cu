@@ -113,17 +113,21 @@ QL_DEVINL int row_exponent(const uint16_t* sw, int g0, int g1, bool vec) {
   return 10 - log2_bf16(min(top, 0x7F7Fu), 10);
 }
 
-// A row's scales and zero points of one weight stage, loaded a stage ahead.
-template <int kGroup, bool kZero>
+// A row's scales and zero points of a weight stage's granules kStep i + first, loaded a
+// stage ahead.
+template <int kGroup, bool kZero, int kStep>
 struct G4Scales {
-  static constexpr int kN = kG4StageK / kGroup;
+  static constexpr int kStage = kG4StageK / kGroup;   // groups of a stage
+  static constexpr int kPer = kGroup == 32 ? 2 : 1;   // groups in a granule
+  static constexpr int kOwn = 4 / kStep;
+  static constexpr int kN = kGroup == 128 ? 2 : kOwn * kPer;
   uint32_t sraw[kN], zraw[kZero ? kN : 1];
   uint32_t s2[kN], z0[kN], z1[kZero ? kN : 1];  // kZero: zlo, zhi; else z0 = -24 s
 
-  QL_DEVINL void load(const uint16_t* sw, const uint8_t* wz, int w, int groups) {
+  QL_DEVINL void load(const uint16_t* sw, const uint8_t* wz, int w, int first, int groups) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int gi = w * kN + i;
+      const int gi = w * kStage + (kGroup == 128 ? i : (kStep * (i / kPer) + first) * kPer + i % kPer);
       sraw[i] = gi < groups ? __ldg(sw + gi) : 0;
       if constexpr (kZero) zraw[i] = gi < groups ? __ldg(wz + gi) : 8;
     }
@@ -149,10 +153,11 @@ struct G4Scales {
     c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w;
     c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
   }
-  QL_DEVINL void granule(const uint32_t (&c)[8], int gq, uint32_t (&h)[32]) const {
+  // The weights of granule kStep own + first.
+  QL_DEVINL void granule(const uint32_t (&c)[8], int own, uint32_t (&h)[32]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int gi = (gq * 64 + i * 8) / kGroup;
+      const int gi = kGroup == 128 ? own * kStep / 2 : own * kPer + i * kPer / 8;
       if constexpr (kZero)
         w4::codes_to_f16_zero(c[i], z0[gi], z1[gi], s2[gi], h + 4 * i);
       else
@@ -343,33 +348,33 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     w4::wait(done, 0, nullptr);
   } else if (count > 0 && warp < kG4DequantWarps) {
     // ------------------------------------------------------------ codes -> TMEM
-    // Warps 0-3 take the even granules, 4-7 the odd ones; thread = weight row.
+    // Warps 0-3 take a stage's even granules, 4-7 the odd ones; thread = weight row.
     const int wg = warp >> 2, q = warp & 3;
     const int64_t n = n0 + q * 32 + lane;
     const int64_t wr = e * p.N + min(n, p.N - 1);
     const uint16_t* sw = p.sw + wr * p.groups;
     const uint8_t* wz = kZero ? p.wz + wr * p.groups : nullptr;
-    G4Scales<kGroup, kZero> sc;
-    const int f = row_exponent(sw, kr.w0 * sc.kN, min(p.groups, (kr.w0 + kr.n) * sc.kN), (p.groups & 7) == 0);
+    G4Scales<kGroup, kZero, 2> sc;
+    const int f = row_exponent(sw, kr.w0 * sc.kStage, min(p.groups, (kr.w0 + kr.n) * sc.kStage), (p.groups & 7) == 0);
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
     const uint32_t row_off = (uint32_t)((q * 32 + lane) * 128);
-    sc.load(sw, wz, kr.stage(0), p.groups);
+    sc.load(sw, wz, kr.stage(0), wg, p.groups);
     bool ok = true;
-    int j = 0;  // granule
+    int j0 = 0;  // the stage's first granule
     for (int jw = 0; jw < kr.n && ok; ++jw) {
       const int ws = jw % kG4WStages, ng = kr.granules(kr.stage(jw));
       sc.convert(f);
-      if (jw + 1 < kr.n) sc.load(sw, wz, kr.stage(jw + 1), p.groups);
+      if (jw + 1 < kr.n) sc.load(sw, wz, kr.stage(jw + 1), wg, p.groups);
       ok = w4::wait(&wfull[ws], (jw / kG4WStages) & 1, abort_flag);
       if (!ok) break;
       const uint8_t* src = wring + ws * kNarrowWBytes + row_off;
 #pragma unroll
-      for (int gq = 0; gq < 4; ++gq, ++j) {
+      for (int i = 0; i < 2; ++i) {
+        const int gq = 2 * i + wg, j = j0 + gq;
         if (gq >= ng) break;
-        if ((j & 1) != wg) continue;
         uint32_t c[8], h[32];
         sc.codes(src, gq, (uint32_t)(lane & 7), c);
-        sc.granule(c, gq, h);
+        sc.granule(c, i, h);
         const int slot = j % kSlots, use = j / kSlots;
         if (use > 0) ok = w4::wait(&aempty[slot], (use - 1) & 1, abort_flag);
         if (!ok) break;
@@ -381,6 +386,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
         if (lane == 0) mbar_arrive(&afull[slot]);
       }
       if (!ok) break;
+      j0 += ng;
       __syncwarp();
       if (lane == 0) mbar_arrive(&wempty[ws]);
     }
@@ -438,12 +444,28 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     }
     if (!*abort_flag) {
       const uint32_t part = smem_u32(wring);
-      for (int i = threadIdx.x; i < 128 * ((count - split + p.splits - 1) / p.splits); i += kThreads) {
-        const int c = (i / 128) * p.splits + split, col = i % 128;
+      const bool vec = (p.N & 3) == 0;
+      for (int i = threadIdx.x; i < 32 * ((count - split + p.splits - 1) / p.splits); i += kThreads) {
+        const int c = (i / 32) * p.splits + split, col = i % 32 * 4;
         if (n0 + col >= p.N) continue;
-        float sum = 0.0f;
-        for (int s = 0; s < p.splits; ++s) sum += w4::ld_cluster(part + (uint32_t)(c * 128 + col) * 4u, (uint32_t)s);
-        p.y[(m0 + c) * p.N + n0 + col] = f32_to_bf16_rn(sum);
+        float4 v[kG4MaxSplit];
+#pragma unroll
+        for (int s = 0; s < kG4MaxSplit; ++s)
+          if (s < p.splits) v[s] = w4::ld_cluster(part + (uint32_t)(c * 128 + col) * 4u, (uint32_t)s);
+        float4 sum = v[0];
+#pragma unroll
+        for (int s = 1; s < kG4MaxSplit; ++s)
+          if (s < p.splits) sum.x += v[s].x, sum.y += v[s].y, sum.z += v[s].z, sum.w += v[s].w;
+        uint16_t* out = p.y + (m0 + c) * p.N + n0 + col;
+        if (vec) {
+          *reinterpret_cast<uint2*>(out) =
+              make_uint2(w4::f32x2_to_bf16x2(sum.x, sum.y), w4::f32x2_to_bf16x2(sum.z, sum.w));
+        } else {
+          const float o[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n0 + col + j < p.N) out[j] = f32_to_bf16_rn(o[j]);
+        }
       }
     }
     __syncwarp();
@@ -683,14 +705,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const int64_t wr = w.e * p.N + min((int64_t)w.rt * 256 + row, p.N - 1);
       const uint16_t* sw = p.sw + wr * p.groups;
       const uint8_t* wz = kZero ? p.wz + wr * p.groups : nullptr;
-      G4Scales<kGroup, kZero> sc;
-      sc.load(sw, wz, kr.stage(0), p.groups);
+      G4Scales<kGroup, kZero, 1> sc;
+      sc.load(sw, wz, kr.stage(0), 0, p.groups);
       const int f = row_exponent(sw, 0, p.groups, (p.groups & 7) == 0);
       s_f[(it & 3) * 256 + row] = f;
       for (int j = 0; j < kr.n && ok; ++j, ++jw) {
         const int ws = jw % kG4WStages, ng = kr.granules(kr.stage(j));
         sc.convert(f);
-        if (j + 1 < kr.n) sc.load(sw, wz, kr.stage(j + 1), p.groups);
+        if (j + 1 < kr.n) sc.load(sw, wz, kr.stage(j + 1), 0, p.groups);
         ok = w4::wait(&wfull[ws], (jw / kG4WStages) & 1, abort_flag);
         if (!ok) break;
         const uint8_t* src = wring + ws * kWideWBytes + row * 128;
@@ -1063,34 +1085,52 @@ struct G4Plan {
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-G4Plan plan_dense(int64_t M, const ql_w4_weight& w, int sms) {
+// One weight tile and K split over clusters: as many CTAs as the SMs hold, two each.
+G4Plan plan_narrow(int64_t M, const ql_w4_weight& w, int sms) {
   G4Plan g;
-  if (M > 128) {
-    g.wide = true;
-    g.row_tiles = (unsigned)div_up(w.N, 256);
-    g.splits = 1;
-    // tokens of a tile: fewest rounds of the SMs, each round's time about its tokens
-    g.ntok = kWideTok;
-    double best = 1e30;
-    for (int n = kWideTok; n >= 96; n -= 16) {
-      const double cost = (double)div_up(g.row_tiles * div_up(M, n), sms) * (n + 16);
-      if (cost < best) {
-        best = cost;
-        g.ntok = n;
-      }
-    }
-    g.tok_tiles = (unsigned)div_up(M, g.ntok);
-  } else {
-    g.wide = false;
-    g.row_tiles = (unsigned)div_up(w.N, 128);
-    g.ntok = (int)div_up(M, 16) * 16;
-    g.tok_tiles = 1;
-    g.splits = 1;
-    const int64_t stages = div_up(w.K, kG4StageK);
-    while (g.splits < kG4MaxSplit && g.splits * 2 <= stages && (int64_t)g.row_tiles * g.splits * 2 <= 2 * sms)
-      g.splits *= 2;
-  }
+  g.wide = false;
+  g.row_tiles = (unsigned)div_up(w.N, 128);
+  g.tok_tiles = (unsigned)div_up(M, kNarrowTok);
+  g.ntok = (int)div_up(div_up(M, g.tok_tiles), 16) * 16;
+  g.splits = 1;
+  const int64_t stages = div_up(w.K, kG4StageK);
+  while (g.splits < kG4MaxSplit && g.splits * 2 <= stages &&
+         (int64_t)g.row_tiles * g.tok_tiles * g.splits * 2 <= 2 * sms)
+    g.splits *= 2;
   return g;
+}
+
+G4Plan plan_wide(int64_t M, const ql_w4_weight& w, int sms) {
+  G4Plan g;
+  g.wide = true;
+  g.row_tiles = (unsigned)div_up(w.N, 256);
+  g.splits = 1;
+  // tokens of a tile: fewest rounds of the SMs, each round's time about its tokens
+  g.ntok = kWideTok;
+  double best = 1e30;
+  for (int n = kWideTok; n >= 96; n -= 16) {
+    const double cost = (double)div_up(g.row_tiles * div_up(M, n), sms) * (n + 16);
+    if (cost < best) {
+      best = cost;
+      g.ntok = n;
+    }
+  }
+  g.tok_tiles = (unsigned)div_up(M, g.ntok);
+  return g;
+}
+
+G4Plan plan_dense(int64_t M, const ql_w4_weight& w, int sms) {
+  const G4Plan n = plan_narrow(M, w, sms);
+  if (M <= kNarrowTok) return n;
+  // Few wide tiles leave SMs without work while each of them walks all of K, whatever its
+  // tokens (about 0.44 us a granule); two narrow tiles on an SM take about 1.25 times that
+  // for theirs (K = 4096, narrow against wide: 129 tokens 4096 rows 17.5 and 33 us, 512
+  // tokens 30.7 and 37.2, 1000 tokens 41.0 and 38.8; 512 tokens 1024 rows 19.9 and 35.2).
+  const G4Plan g = plan_wide(M, w, sms);
+  const int64_t gran = div_up(w.K, kG4GranK);
+  const double wide = (double)div_up((int64_t)g.row_tiles * g.tok_tiles, sms) * gran;
+  const double narrow = 1.25 * div_up((int64_t)n.row_tiles * n.tok_tiles * n.splits, 2 * sms) * div_up(gran, n.splits);
+  return narrow < wide ? n : g;
 }
 
 G4Plan plan_experts_host(int64_t pairs, const ql_w4_weight& w) {

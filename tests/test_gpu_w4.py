@@ -53,7 +53,8 @@ def test_product(cuda, group, zeros, M, N, K):
 @pytest.mark.parametrize("M,N,K,group,zeros", [
     (1, 1024, 4096, 128, False), (3, 4096, 14336, 128, True), (12, 14336, 4096, 64, False), (24, 4096, 4096, 32, True),
     (512, 1024, 4096, 128, False), (1, 4096, 4096, 32, True), (8, 6144, 4096, 64, True), (16, 4096, 4160, 128, True),
-    (2, 5003, 4128, 128, False), (9, 14336, 992, 32, False)])
+    (2, 5003, 4128, 128, False), (9, 14336, 992, 32, False), (300, 14336, 992, 64, True), (1030, 8197, 512, 128, False),
+    (400, 20001, 160, 32, True), (130, 4096, 4096, 64, True), (300, 1030, 4128, 32, False)])
 def test_product_layer_sizes(cuda, M, N, K, group, zeros):
     """Decoder layer sizes, and the same call twice in one workspace gives the same bits."""
     x, wq, sw, wz = _case(M, N, K, group, zeros)
@@ -71,7 +72,8 @@ def test_no_tokens(cuda):
     assert y.shape == (0, 64)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 70, 512), (12, 70, 512), (40, 70, 512), (3, 4096, 4096), (16, 4096, 4096)])
+@pytest.mark.parametrize("M,N,K", [(1, 70, 512), (12, 70, 512), (40, 70, 512), (3, 4096, 4096), (16, 4096, 4096),
+                                   (300, 70, 512), (300, 10000, 512)])
 def test_wide_range(cuda, M, N, K):
     """Scales 2^-100 .. 2^20 in one row, tokens 2^-60 .. 2^60 apart: nothing is lost
     to the operands' range."""
@@ -115,7 +117,8 @@ def test_row_results_do_not_depend_on_the_batch(cuda):
     assert torch.equal(ql.forward_w4(x[:1].cuda(), w), full[:1])
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 144, 384), (16, 144, 384), (50, 144, 384), (5, 4096, 4096), (300, 520, 384)])
+@pytest.mark.parametrize("M,N,K", [(1, 144, 384), (16, 144, 384), (50, 144, 384), (5, 4096, 4096), (300, 520, 384),
+                                   (300, 10000, 384)])
 def test_side_stream_and_graph(cuda, M, N, K):
     """On another stream than the current one, and captured: the replay reads the
     inputs, the weights and the zero points as they are then."""
