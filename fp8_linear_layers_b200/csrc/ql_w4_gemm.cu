@@ -859,6 +859,19 @@ struct G4PrepParams {
   int64_t N;
 };
 
+// do_(pair, its expert or -1) for this thread's pairs, eight loads in flight.
+template <class Do>
+QL_DEVINL void each_id(const G4PrepParams& p, Do do_) {
+  for (int64_t i0 = threadIdx.x; i0 < p.pairs; i0 += 8 * kG4PlanThreads) {
+    int e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = i0 + j * kG4PlanThreads < p.pairs ? __ldg(p.ids + i0 + j * kG4PlanThreads) : -1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i0 + j * kG4PlanThreads < p.pairs) do_(i0 + j * kG4PlanThreads, e[j] < p.E ? e[j] : -1);
+  }
+}
+
 // Cuts the experts' pairs, in expert order, into token tiles; one thread per expert.
 // Returns the first place of expert threadIdx.x's pairs.
 QL_DEVINL int plan_tiles(const G4PrepParams& p, int* hist) {
@@ -866,10 +879,9 @@ QL_DEVINL int plan_tiles(const G4PrepParams& p, int* hist) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   hist[tid] = 0;
   __syncthreads();
-  for (int64_t i = tid; i < p.pairs; i += kG4PlanThreads) {
-    const int e = p.ids[i];
-    if (e >= 0 && e < p.E) atomicAdd(&hist[e], 1);
-  }
+  each_id(p, [&](int64_t, int e) {
+    if (e >= 0) atomicAdd(&hist[e], 1);
+  });
   __syncthreads();
   // exclusive sums of the pairs and of the tiles
   const int c = hist[tid], t = (c + p.ntok - 1) / p.ntok;
@@ -922,32 +934,65 @@ __global__ void __launch_bounds__(kG4PlanThreads) w4_plan_kernel(const G4PrepPar
   __syncthreads();
   hist[threadIdx.x] = base;
   __syncthreads();
-  for (int64_t i = threadIdx.x; i < p.pairs; i += kG4PlanThreads) {
-    const int e = p.ids[i];
-    p.pos[i] = e >= 0 && e < p.E ? atomicAdd(&hist[e], 1) : -1;
-  }
+  each_id(p, [&](int64_t i, int e) { p.pos[i] = e >= 0 ? atomicAdd(&hist[e], 1) : -1; });
 }
 
-// The power of two of a row of tokens: its largest finite |x| to [2^14, 2^15).
-QL_DEVINL int token_exponent(const uint4* src, int chunks, uint32_t* red) {
-  uint32_t top = 0;
-  for (int i = threadIdx.x; i < chunks; i += blockDim.x) {
-    const uint4 v = __ldg(src + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// The largest finite magnitude of eight inputs and `top`.
+QL_DEVINL uint32_t largest8(const uint4& v, uint32_t top) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t a = w[j] & 0x7FFFu, b = w[j] >> 16 & 0x7FFFu;
-      if (a < 0x7F80u) top = max(top, a);
-      if (b < 0x7F80u) top = max(top, b);
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t a = w[j] & 0x7FFFu, b = w[j] >> 16 & 0x7FFFu;
+    if (a < 0x7F80u) top = max(top, a);
+    if (b < 0x7F80u) top = max(top, b);
+  }
+  return top;
+}
+
+// A row of x for the threads of a warp (kBlock false) or of a block, held in registers
+// (kHold pieces a thread) from the search for its largest value to its conversion; a
+// longer row's rest is read twice.
+template <bool kBlock, int kHold>
+struct G4Row {
+  const uint4* src;
+  int chunks, first, step;  // pieces of 8 inputs, this thread's first, and from one to the next
+  uint4 v[kHold];
+
+  QL_DEVINL G4Row(const uint16_t* row, int64_t K)
+      : src(reinterpret_cast<const uint4*>(row)),
+        chunks((int)(K / 8)),
+        first(kBlock ? threadIdx.x : threadIdx.x & 31),
+        step(kBlock ? blockDim.x : 32) {
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (first + i * step < chunks) v[i] = __ldg(src + first + i * step);
     }
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
-  __syncthreads();
-  top = 0;
-  for (int i = 0; i < (int)blockDim.x / 32; ++i) top = max(top, red[i]);
-  return 14 - log2_bf16(top, 14);
-}
+  // The power of two that brings the row's largest finite |x| to [2^14, 2^15).
+  QL_DEVINL int exponent(uint32_t* red) const {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) top = largest8(v[i], top);
+    for (int i = first + kHold * step; i < chunks; i += step) top = largest8(__ldg(src + i), top);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if constexpr (kBlock) {
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+      __syncthreads();
+      top = 0;
+      for (int i = 0; i < (int)blockDim.x / 32; ++i) top = max(top, red[i]);
+    }
+    return 14 - log2_bf16(top, 14);
+  }
+  // store(piece, its number) for this thread's pieces.
+  template <class Store>
+  QL_DEVINL void each(Store store) const {
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (first + i * step < chunks) store(v[i], first + i * step);
+    for (int i = first + kHold * step; i < chunks; i += step) store(__ldg(src + i), i);
+  }
+};
 
 // Eight inputs scaled by f0 f1, in the order 0 4 1 5 2 6 3 7.
 QL_DEVINL uint4 prepare8(const uint4& v, float f0, float f1) {
@@ -967,13 +1012,25 @@ __global__ void __launch_bounds__(kG4PrepThreads) w4_prepare_kernel(const G4Prep
   tc::grid_dependency_wait();
   tc::launch_dependents();
   const int64_t row = blockIdx.x;
-  const uint4* src = reinterpret_cast<const uint4*>(p.x + row * p.K);
-  const int chunks = (int)(p.K / 8);
-  const int e = token_exponent(src, chunks, red);
+  const G4Row<true, 4> x(p.x + row * p.K, p.K);
+  const int e = x.exponent(red);
   if (threadIdx.x == 0) p.ex[row] = e;
   const float f0 = exp2i(e / 2), f1 = exp2i(e - e / 2);
   uint4* dst = reinterpret_cast<uint4*>(p.x16 + row * p.K);
-  for (int i = threadIdx.x; i < chunks; i += kG4PrepThreads) dst[i] = prepare8(__ldg(src + i), f0, f1);
+  x.each([&](const uint4& v, int i) { dst[i] = prepare8(v, f0, f1); });
+}
+
+// A pair's place in expert order (-1: no expert), counted by its warp.
+QL_DEVINL int count_place(const G4PrepParams& p, int pair) {
+  const int e = __ldg(p.ids + pair);
+  int before = 0;
+#pragma unroll 8
+  for (int i = threadIdx.x & 31; i < (int)p.pairs; i += 32) {
+    const int o = __ldg(p.ids + i);
+    before += (o >= 0 && o < e) || (o == e && i < pair);
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  return e >= 0 && e < p.E ? before : -1;
 }
 
 // Experts: a block takes an x row and writes it once for each of its pairs, in expert
@@ -994,39 +1051,55 @@ __global__ void __launch_bounds__(kG4PlanThreads) w4_prepare_experts_kernel(cons
       return;
     }
     --row;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int j = warp; j < p.slots; j += blockDim.x / 32) {
-      const int pair = (int)row * p.slots + j, e = p.ids[pair];
-      int before = 0;
-      for (int i = lane; i < (int)p.pairs; i += 32) {
-        const int o = p.ids[i];
-        before += (o >= 0 && o < e) || (o == e && i < pair);
-      }
-      before = __reduce_add_sync(0xffffffffu, before);
-      if (lane == 0) s_pos[j] = e >= 0 && e < p.E ? before : -1;
+    for (int j = threadIdx.x >> 5; j < p.slots; j += blockDim.x / 32) {
+      const int pos = count_place(p, (int)row * p.slots + j);
+      if ((threadIdx.x & 31) == 0) s_pos[j] = pos;
     }
   } else if (threadIdx.x < p.slots) {
     s_pos[threadIdx.x] = p.pos[row * p.slots + threadIdx.x];
   }
-  const uint4* src = reinterpret_cast<const uint4*>(p.x + row * p.K);
-  const int chunks = (int)(p.K / 8);
-  const int e = token_exponent(src, chunks, red);  // (and a barrier behind s_pos)
+  const G4Row<true, 1> x(p.x + row * p.K, p.K);
+  const int e = x.exponent(red);  // (and a barrier behind s_pos)
   const float f0 = exp2i(e / 2), f1 = exp2i(e - e / 2);
   if (threadIdx.x < p.slots && s_pos[threadIdx.x] >= 0) {
     p.ex[s_pos[threadIdx.x]] = e;
     p.order[s_pos[threadIdx.x]] = (int)row * p.slots + threadIdx.x;
   }
-  for (int i = threadIdx.x; i < chunks; i += blockDim.x) {
-    const uint4 v = prepare8(__ldg(src + i), f0, f1);
+  x.each([&](const uint4& v, int i) {
+    const uint4 h = prepare8(v, f0, f1);
     for (int j = 0; j < p.slots; ++j)
-      if (s_pos[j] >= 0) reinterpret_cast<uint4*>(p.x16 + (int64_t)s_pos[j] * p.K)[i] = v;
-  }
+      if (s_pos[j] >= 0) reinterpret_cast<uint4*>(p.x16 + (int64_t)s_pos[j] * p.K)[i] = h;
+  });
   if (p.zero_y) {
     for (int j = 0; j < p.slots; ++j) {
       if (s_pos[j] >= 0) continue;
       for (int64_t n = threadIdx.x; n < p.N; n += blockDim.x) p.zero_y[(row * p.slots + j) * p.N + n] = 0;
     }
   }
+}
+
+// Pairs with an x row each: a warp takes a row.
+__global__ void __launch_bounds__(kG4PlanThreads) w4_prepare_pairs_kernel(const G4PrepParams p) {
+  __shared__ int hist[kG4PlanThreads];
+  tc::grid_dependency_wait();
+  tc::launch_dependents();
+  if (!p.pos && blockIdx.x == 0) {
+    plan_tiles(p, hist);
+    return;
+  }
+  const int64_t row = (int64_t)(blockIdx.x - (p.pos ? 0 : 1)) * (blockDim.x / 32) + (threadIdx.x >> 5);
+  if (row >= p.pairs) return;
+  const int pos = p.pos ? p.pos[row] : count_place(p, (int)row);
+  const G4Row<false, 4> x(p.x + row * p.K, p.K);
+  if (pos < 0) return;
+  const int e = x.exponent(nullptr);
+  const float f0 = exp2i(e / 2), f1 = exp2i(e - e / 2);
+  if ((threadIdx.x & 31) == 0) {
+    p.ex[pos] = e;
+    p.order[pos] = (int)row;
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.x16 + (int64_t)pos * p.K);
+  x.each([&](const uint4& v, int i) { dst[i] = prepare8(v, f0, f1); });
 }
 
 // y[t] = sum_j weights[t, j] yp[t, j], the pairs' products rounded to bf16 (half the
@@ -1044,22 +1117,29 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(const uint16_t* __restr
   float sum[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) sum[i] = 0.0f;
-#pragma unroll 4
-  for (int j = 0; j < topk; ++j) {
-    const int e = __ldg(ids + t * topk + j);
-    if (e < 0 || e >= E) continue;
-    const float w = __ldg(weights + t * topk + j);
-    const uint16_t* src = yp + (t * topk + j) * N + n;
-    if constexpr (kVec == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(src);
-      const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+  constexpr int kAhead = 8;  // pairs whose products are loaded before the first is added
+  for (int j0 = 0; j0 < topk; j0 += kAhead) {
+    float w[kAhead];
+    bool use[kAhead];
+    uint4 v[kAhead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sum[2 * i] = fmaf(w, bf16_lo(q[i]), sum[2 * i]);
-        sum[2 * i + 1] = fmaf(w, bf16_hi(q[i]), sum[2 * i + 1]);
-      }
-    } else {
-      sum[0] = fmaf(w, bf16_lo(*src), sum[0]);
+    for (int j = 0; j < kAhead; ++j) {
+      const int e = j0 + j < topk ? __ldg(ids + t * topk + j0 + j) : -1;
+      use[j] = e >= 0 && e < E;
+      w[j] = use[j] ? __ldg(weights + t * topk + j0 + j) : 0.0f;
+      if (!use[j]) continue;  // (not a product with zero: the place holds anything)
+      const uint16_t* src = yp + (t * topk + j0 + j) * N + n;
+      if constexpr (kVec == 8)
+        v[j] = *reinterpret_cast<const uint4*>(src);
+      else
+        v[j].x = *src;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (!use[j]) continue;
+      const uint32_t q[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) sum[i] = fmaf(w[j], i % 2 ? bf16_hi(q[i / 2]) : bf16_lo(q[i / 2]), sum[i]);
     }
   }
   if constexpr (kVec == 8) {
@@ -1318,13 +1398,14 @@ cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float
   q.zero_y = combine ? nullptr : y;
   q.N = w.N;
   cudaError_t e;
-  const unsigned rows = (unsigned)(combine ? pairs : T);
   if (pairs > kG4CountPairs) {
     q.pos = reinterpret_cast<int*>(ws + L.pos);
     if ((e = launch_pdl(w4_plan_kernel, 1, kG4PlanThreads, q, st)) != cudaSuccess) return e;
-    e = launch_pdl(w4_prepare_experts_kernel, rows, 256, q, st);
+    e = combine ? launch_pdl(w4_prepare_pairs_kernel, (unsigned)div_up(pairs, 8), 256, q, st)
+                : launch_pdl(w4_prepare_experts_kernel, (unsigned)T, 256, q, st);
   } else {
-    e = launch_pdl(w4_prepare_experts_kernel, rows + 1, kG4PlanThreads, q, st);
+    e = combine ? launch_pdl(w4_prepare_pairs_kernel, (unsigned)div_up(pairs, kG4PlanThreads / 32) + 1, kG4PlanThreads, q, st)
+                : launch_pdl(w4_prepare_experts_kernel, (unsigned)T + 1, kG4PlanThreads, q, st);
   }
   if (e != cudaSuccess) return e;
   uint16_t* yp = combine ? reinterpret_cast<uint16_t*>(ws + L.yp) : y;
