@@ -181,7 +181,7 @@ struct G4Range {
 
 // ---------------------------------------------------------------------------- narrow
 
-template <int kGroup, bool kZero, bool kExperts>
+template <int kGroup, bool kZero>
 __global__ void __launch_bounds__(kNarrowThreads, 2)
     w4_narrow_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                      const G4Params p) {
@@ -200,8 +200,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   uint64_t* aempty = afull + kSlots;
   uint64_t* done = aempty + kSlots;
   int* s_ex = reinterpret_cast<int*>(done + 2);               // the columns' exponents (16-byte aligned)
-  int* s_out = s_ex + kNarrowTok;                              // experts: pairs
-  float* s_fac = reinterpret_cast<float*>(s_out + kNarrowTok); // 2^-exponent
+  float* s_fac = reinterpret_cast<float*>(s_ex + kNarrowTok); // 2^-exponent
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_fac + kNarrowTok);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_wide = reinterpret_cast<int*>(tmem_holder + 2);  // an exponent that one factor cannot take
@@ -245,21 +244,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   tc::launch_dependents();
 
   // this CTA's tokens: exponent, and as a factor 2^-ex
-  int64_t e = 0, m0 = 0;
-  int count;
-  if constexpr (kExperts) {
-    const bool live = (int)blockIdx.y < *p.ntiles;
-    const G4Tile tile = live ? p.tiles[blockIdx.y] : G4Tile{0, 0, 0, 0};
-    e = tile.expert;
-    count = tile.count;
-    m0 = tile.start;
-  } else {
-    m0 = (int64_t)blockIdx.y * p.ntok;
-    count = (int)min((int64_t)p.ntok, p.M - m0);
-  }
+  const int64_t m0 = (int64_t)blockIdx.y * p.ntok;
+  const int count = (int)min((int64_t)p.ntok, p.M - m0);
   for (int i = threadIdx.x; i < count; i += kThreads) {
     const int ex = p.ex[m0 + i];
-    if constexpr (kExperts) s_out[i] = p.order[m0 + i];
     s_ex[i] = ex;
     s_fac[i] = exp2i(max(-126, min(126, -ex)));
     if (abs(ex) > 60) *s_wide = 1;
@@ -271,11 +259,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   const uint32_t tmem_a = tmem + 128;
   const int mma_n = (count + 15) & ~15;
 
-  if (count > 0 && warp == kG4DequantWarps) {
+  if (warp == kG4DequantWarps) {
     // ------------------------------------------------------------ TMA producer
     const uint64_t pol_w = l2_policy_evict_first();
     const uint64_t pol_x = l2_policy_evict_last();
-    const int wrow = (int)(e * p.N + n0);
+    const int wrow = (int)n0;
     bool ok = true;
     int jw = 0, jx = 0;  // issued stages
     int s = 0;           // token stage of the next granule, and how often it was filled
@@ -313,7 +301,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
         mbar_wait_bounded(&wfull[j % kG4WStages], (j / kG4WStages) & 1, nullptr);
       for (int j = max(0, jx - xs_n); j < jx; ++j) mbar_wait_bounded(&xfull[j % xs_n], (j / xs_n) & 1, nullptr);
     }
-  } else if (count > 0 && warp == kMmaWarp) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t id = w4::idesc_f16(128, mma_n);
     const uint32_t elected = w4::elect_one();
@@ -346,12 +334,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     }
     w4::commit(done, elected);
     w4::wait(done, 0, nullptr);
-  } else if (count > 0 && warp < kG4DequantWarps) {
+  } else if (warp < kG4DequantWarps) {
     // ------------------------------------------------------------ codes -> TMEM
     // Warps 0-3 take a stage's even granules, 4-7 the odd ones; thread = weight row.
     const int wg = warp >> 2, q = warp & 3;
     const int64_t n = n0 + q * 32 + lane;
-    const int64_t wr = e * p.N + min(n, p.N - 1);
+    const int64_t wr = min(n, p.N - 1);
     const uint16_t* sw = p.sw + wr * p.groups;
     const uint8_t* wz = kZero ? p.wz + wr * p.groups : nullptr;
     G4Scales<kGroup, kZero, 2> sc;
@@ -478,13 +466,13 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
       tc::fence_after();
       tc::tmem_dealloc(tmem, 256);
     }
-    if (count > 0 && !*abort_flag) {
+    if (!*abort_flag) {
       constexpr int kRow = 128 * 2 + 16;
       const int cols = (int)min((int64_t)128, p.N - n0);
       if ((p.N & 7) == 0) {
         for (int i = threadIdx.x; i < count * 16; i += kThreads) {
           const int c = i / 16, b = i % 16;
-          const int64_t row = kExperts ? s_out[c] : m0 + c;
+          const int64_t row = m0 + c;
           if (b * 8 < cols)
             *reinterpret_cast<uint4*>(p.y + row * p.N + n0 + b * 8) =
                 *reinterpret_cast<const uint4*>(wring + c * kRow + b * 16);
@@ -492,7 +480,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
       } else {
         for (int i = threadIdx.x; i < count * 128; i += kThreads) {
           const int c = i / 128, b = i % 128;
-          const int64_t row = kExperts ? s_out[c] : m0 + c;
+          const int64_t row = m0 + c;
           if (b < cols) p.y[row * p.N + n0 + b] = *reinterpret_cast<const uint16_t*>(wring + c * kRow + b * 2);
         }
       }
@@ -1210,16 +1198,22 @@ G4Plan plan_dense(int64_t M, const ql_w4_weight& w, int sms) {
   const int64_t gran = div_up(w.K, kG4GranK);
   const double wide = (double)div_up((int64_t)g.row_tiles * g.tok_tiles, sms) * gran;
   const double narrow = 1.25 * div_up((int64_t)n.row_tiles * n.tok_tiles * n.splits, 2 * sms) * div_up(gran, n.splits);
-  return narrow < wide ? n : g;
+  return narrow < wide && n.tok_tiles <= 65535u ? n : g;
 }
 
-G4Plan plan_experts_host(int64_t pairs, const ql_w4_weight& w) {
+// Experts always take wide tiles (64 experts, 8 to a token: 2048 x 768 combined 20 tokens
+// 26 us against 32 in narrow ones, 256 tokens 41 against 48; 1536 x 2048 512 tokens 62
+// against 82).  A tile's token loads are ntok rows whatever its expert has, and an expert
+// with more takes another tile: four times the mean of the pairs up to 128 (1536 x 2048,
+// 256 tokens, mean 32: 48 rows 67 us, 128 rows 56; 64 tokens, mean 8: 32 rows 50), then 192
+// (2048 x 768, mean 127: 128 rows 69 us, 192 rows 66).
+G4Plan plan_experts(int64_t pairs, const ql_w4_weight& w) {
   G4Plan g;
   const int64_t per = div_up(pairs, w.experts);
   g.splits = 1;
-  g.wide = per > 64;
-  g.row_tiles = (unsigned)div_up(w.N, g.wide ? 256 : 128);
-  g.ntok = g.wide ? kWideTok : per > 16 ? 64 : 32;
+  g.wide = true;
+  g.row_tiles = (unsigned)div_up(w.N, 256);
+  g.ntok = per > 80 ? kWideTok : (int)std::min<int64_t>(128, std::max<int64_t>(32, div_up(per, 4) * 16));
   g.tok_tiles = (unsigned)(std::min<int64_t>(w.experts, pairs) + pairs / g.ntok);
   return g;
 }
@@ -1277,20 +1271,22 @@ template <int kGroup, bool kZero, bool kExperts>
 cudaError_t launch_g4_t(const CUtensorMap& tw, const CUtensorMap& tx, const G4Params& p, const G4Plan& g, int sms,
                         cudaStream_t st) {
   const int ring = kG4WStages * (g.wide ? kWideWBytes : kNarrowWBytes) + p.xstages * p.xstage;
-  if (g.wide) {
-    const int smem = 1024 + ring + kWideEpiWarps * 16 * kWideStageRow + 32 * 8 + 4 * 256 * 4 + 6 * kWideTok * 4 + 16;
-    const unsigned grid = (unsigned)std::min<int64_t>(sms, (int64_t)g.row_tiles * g.tok_tiles);
-    return launch_g4_kernel<w4_wide_kernel<kGroup, kZero, kExperts>>(tw, tx, p, dim3(grid), kWideThreads, smem, st);
+  if constexpr (!kExperts) {
+    if (!g.wide) {
+      const int smem = 1024 + ring + 8 * (2 * kG4WStages + 2 * kG4MaxXStages + 2 * kNarrowSlots + 2) + 8 * kNarrowTok + 16;
+      return launch_g4_kernel<w4_narrow_kernel<kGroup, kZero>>(tw, tx, p, dim3(g.row_tiles * g.splits, g.tok_tiles),
+                                                               kNarrowThreads, smem, st);
+    }
   }
-  const int smem = 1024 + ring + 8 * (2 * kG4WStages + 2 * kG4MaxXStages + 2 * kNarrowSlots + 2) + 12 * kNarrowTok + 16;
-  return launch_g4_kernel<w4_narrow_kernel<kGroup, kZero, kExperts>>(
-      tw, tx, p, dim3(g.row_tiles * g.splits, g.tok_tiles), kNarrowThreads, smem, st);
+  const int smem = 1024 + ring + kWideEpiWarps * 16 * kWideStageRow + 32 * 8 + 4 * 256 * 4 + 6 * kWideTok * 4 + 16;
+  const unsigned grid = (unsigned)std::min<int64_t>(sms, (int64_t)g.row_tiles * g.tok_tiles);
+  return launch_g4_kernel<w4_wide_kernel<kGroup, kZero, kExperts>>(tw, tx, p, dim3(grid), kWideThreads, smem, st);
 }
 
 template <bool kExperts>
 cudaError_t launch_g4(const ql_w4_weight& w, const uint16_t* x16, int64_t rows, G4Params p, const G4Plan& g, int sms,
                       cudaStream_t st) {
-  if (g.tok_tiles > 65535u || (int64_t)g.tok_tiles * g.row_tiles >= (int64_t(1) << 31)) return cudaErrorNotSupported;
+  if ((int64_t)g.tok_tiles * g.row_tiles >= (int64_t(1) << 31)) return cudaErrorNotSupported;
   CUtensorMap tw, tx;
   cudaError_t e = make_tmap_u8_sw128(&tw, w.wq, (uint64_t)w.K / 2, (uint64_t)w.experts * w.N, (uint64_t)w.K / 2, 128, 128);
   if (e != cudaSuccess) return e;
@@ -1369,7 +1365,7 @@ cudaError_t launch_w4(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint1
 size_t w4_experts_workspace_bytes(int64_t T, int64_t topk, const ql_w4_weight& w, bool combine, int sms) {
   if (T <= kW4StreamMaxExpertTokens) return 0;
   const int64_t pairs = T * topk;
-  const G4Plan g = plan_experts_host(pairs, w);
+  const G4Plan g = plan_experts(pairs, w);
   return g4_layout(pairs, w.K, pairs, g.tok_tiles, combine ? pairs * w.N : 0).total;
 }
 
@@ -1379,7 +1375,7 @@ cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float
   if (T <= kW4StreamMaxExpertTokens) return launch_w4_stream_experts(x, ids, weights, w, T, topk, y, sms, st);
   const bool combine = weights != nullptr;
   const int64_t pairs = T * topk;
-  const G4Plan g = plan_experts_host(pairs, w);
+  const G4Plan g = plan_experts(pairs, w);
   const G4Layout L = g4_layout(pairs, w.K, pairs, g.tok_tiles, combine ? pairs * w.N : 0);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   G4PrepParams q = {};
