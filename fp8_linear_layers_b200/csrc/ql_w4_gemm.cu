@@ -44,9 +44,10 @@ constexpr int kWideTok = 192;
 constexpr int kWideRing = 110592;  // bytes of token stages
 constexpr int kWideProducer = kG4DequantWarps;
 constexpr int kWideMma = kWideProducer + 1;
-constexpr int kWideFirstEpi = kWideMma + 1;
+constexpr int kWideFirstEpi = kWideMma + 2;
 constexpr int kWideEpiWarps = 8;
 constexpr int kWideThreads = (kWideFirstEpi + kWideEpiWarps) * 32;
+constexpr int kWideBarriers = 2 * kG4WStages + 2 * kG4MaxXStages + 12;
 constexpr int kWideStageRow = 80;  // bytes of a token in an epilogue warp's staging (32 outputs and a pad)
 constexpr int kWideWBytes = 2 * 128 * 128;
 
@@ -539,12 +540,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   uint64_t* xfull = wempty + kG4WStages;
   uint64_t* xempty = xfull + kG4MaxXStages;
   uint64_t* afull = xempty + kG4MaxXStages;
-  uint64_t* aempty = afull + 2;
-  uint64_t* dfull = aempty + 2;
-  uint64_t* dempty = dfull + 1;
+  uint64_t* aempty = afull + 4;  // (afull, aempty: [row tile][slot]; dfull, dempty: [row tile])
+  uint64_t* dfull = aempty + 4;
+  uint64_t* dempty = dfull + 2;
   // [4][256] the rows' exponents: with short K the dequantizing warps are up to three
   // tiles ahead of the epilogue
-  int* s_f = reinterpret_cast<int*>(wfull + 32);
+  int* s_f = reinterpret_cast<int*>(wfull + kWideBarriers);
   int* s_out = s_f + 4 * 256;                                     // [2][kWideTok] experts: pairs
   int* s_ex = s_out + 2 * kWideTok;                               // [2][kWideTok] the columns' exponents
   float* s_fac = reinterpret_cast<float*>(s_ex + 2 * kWideTok);   // [2][kWideTok] 2^-exponent
@@ -564,14 +565,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     for (int s = 0; s < xs_n; ++s) {
       mbar_init(&xfull[s], 1);
-      mbar_init(&xempty[s], 1);
+      mbar_init(&xempty[s], 2);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&afull[s], kG4DequantWarps);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&afull[s], 4);
       mbar_init(&aempty[s], 1);
     }
-    mbar_init(dfull, 1);
-    mbar_init(dempty, kWideEpiWarps);
+    for (int r = 0; r < 2; ++r) {
+      mbar_init(&dfull[r], 1);
+      mbar_init(&dempty[r], kWideEpiWarps / 2);
+    }
     *abort_flag = 0;
     fence_barrier_init();
     tc::prefetch_tmap(&tmW);
@@ -638,10 +641,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         mbar_wait_bounded(&wfull[j % kG4WStages], (j / kG4WStages) & 1, nullptr);
       for (int j = max(0, jx - xs_n); j < jx; ++j) mbar_wait_bounded(&xfull[j % xs_n], (j / xs_n) & 1, nullptr);
     }
-  } else if (warp == kWideMma) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp == kWideMma || warp == kWideMma + 1) {
+    // ------------------------------------------------------------ MMA issuers, one to a row tile
+    const int r = warp - kWideMma;
     const uint32_t elected = w4::elect_one();
-    const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0), a = d + 2 * kWideTok;  // warp-uniform
+    const uint32_t tmem_a0 = __shfl_sync(0xffffffffu, tmem_a, 0);
+    const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0) + r * kWideTok, a = tmem_a0 + r * 64;  // warp-uniform
     const uint32_t x0 = smem_u32(xring);
     const int ngran = kr.total();
     int xs = 0, g = 0, it = 0;  // g: granules over all tiles
@@ -649,21 +654,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++it) {
       const WideTile w = wide_tile<kExperts>(p, t);
       const uint32_t id = w4::idesc_f16(128, (w.count + 15) & ~15);
-      if (it > 0) ok = w4::wait(dempty, (it - 1) & 1, abort_flag);  // the last tile's sums are read
+      if (it > 0) ok = w4::wait(&dempty[r], (it - 1) & 1, abort_flag);  // the last tile's sums are read
       for (int j = 0; j < ngran && ok; ++j, ++g) {
         const int slot = g & 1;
         ok = w4::wait(&xfull[xs], xphase, abort_flag);
-        ok = ok && w4::wait(&afull[slot], (g >> 1) & 1, abort_flag);
+        ok = ok && w4::wait(&afull[r * 2 + slot], (g >> 1) & 1, abort_flag);
         if (!ok) break;
         tc::fence_after();
         const uint64_t bdesc = tc::sw128_desc(x0 + xs * p.xstage);
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w4::mma_f16_ts(d + r * kWideTok, a + (r * 2 + slot) * 32 + k * 8, bdesc + 2 * k, id, j > 0 || k > 0,
-                           elected);
-        w4::commit(&aempty[slot], elected);
+        for (int k = 0; k < 4; ++k) w4::mma_f16_ts(d, a + slot * 32 + k * 8, bdesc + 2 * k, id, j > 0 || k > 0, elected);
+        w4::commit(&aempty[r * 2 + slot], elected);
         w4::commit(&xempty[xs], elected);
         if (++xs == xs_n) {
           xs = 0;
@@ -671,14 +672,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
       }
       if (!ok) break;
-      w4::commit(dfull, elected);
+      w4::commit(&dfull[r], elected);
     }
     if (!ok) {
       if (lane == 0 && !*abort_flag) record_timeout(p.status, KID_W4, 5);
       *abort_flag = 1;
       // the products in flight end before the CTA leaves
-      w4::commit(dfull, elected);
-      w4::wait(dfull, it & 1, nullptr);
+      w4::commit(&dfull[r], elected);
+      w4::wait(&dfull[r], it & 1, nullptr);
     }
   } else if (warp < kG4DequantWarps) {
     // ------------------------------------------------------------ codes -> TMEM
@@ -713,14 +714,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           sc.granule(c, gq, h);
           if (gq < 3) sc.codes(src, gq + 1, (uint32_t)(lane & 7), c);
           const int slot = g & 1, use = g >> 1;
-          if (use > 0) ok = w4::wait(&aempty[slot], (use - 1) & 1, abort_flag);
+          if (use > 0) ok = w4::wait(&aempty[r * 2 + slot], (use - 1) & 1, abort_flag);
           if (!ok) break;
           tc::fence_after();
           w4::st32(tmem_a + (r * 2 + slot) * 32 + lane_addr, h);
           w4::st_wait();
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&afull[slot]);
+          if (lane == 0) mbar_arrive(&afull[r * 2 + slot]);
           ++g;
         }
         if (!ok) break;
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         wide = abs(ex) > 60;
       }
       wide = wide_epi_any(wide);  // an exponent that one factor cannot take
-      ok = w4::wait(dfull, it & 1, abort_flag);
+      ok = w4::wait(&dfull[r], it & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok && !*abort_flag);
       if (wide_epi_any(!ok)) break;
       tc::fence_after();
@@ -773,7 +774,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (c + 16 >= mma_n) {
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(dempty);
+          if (lane == 0) mbar_arrive(&dempty[r]);
         }
         float o[16];
         if (!wide) {
@@ -1278,7 +1279,7 @@ cudaError_t launch_g4_t(const CUtensorMap& tw, const CUtensorMap& tx, const G4Pa
                                                                kNarrowThreads, smem, st);
     }
   }
-  const int smem = 1024 + ring + kWideEpiWarps * 16 * kWideStageRow + 32 * 8 + 4 * 256 * 4 + 6 * kWideTok * 4 + 16;
+  const int smem = 1024 + ring + kWideEpiWarps * 16 * kWideStageRow + kWideBarriers * 8 + 4 * 256 * 4 + 6 * kWideTok * 4 + 16;
   const unsigned grid = (unsigned)std::min<int64_t>(sms, (int64_t)g.row_tiles * g.tok_tiles);
   return launch_g4_kernel<w4_wide_kernel<kGroup, kZero, kExperts>>(tw, tx, p, dim3(grid), kWideThreads, smem, st);
 }
