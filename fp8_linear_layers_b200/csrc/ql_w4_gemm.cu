@@ -21,6 +21,19 @@
 // A prepare kernel makes the f16 tokens (the inputs of each eight in the order 0 4 1 5
 // 2 6 3 7 in which codes_to_f16 gives the weights) and, for experts, sorts the (token,
 // slot) pairs by expert and cuts each expert's pairs into token tiles.
+//
+// Two kernels.  The narrow one (a 128-row tile, up to 128 tokens, K split over a cluster)
+// gives every SM a share of the weights where there are few tokens; the wide one (256 rows
+// x up to 192 tokens, persistent) converts each weight once for more tokens.  The tensor
+// pipe alone takes 97 cycles for an MMA of 192 columns (96 at its rate); a granule of 64
+// inputs of a wide tile, 640 cycles of MMA at 160 tokens, takes about 760: conversion,
+// tcgen05.st and the four hand-overs between the warps follow one another through two TMEM
+// slots.  Leaving out the conversion saved 19 % of a prompt's time, the stores 29 %, the
+// products 21 %, the token loads 10 %: no single part bounds it.  Tried and slower: four
+// slots (128 tokens), 16 converting warps, outputs held in the epilogue's registers, a
+// store's completion awaited one granule later, one-lane waits.
+// 14336 x 4096, group 128: 2048 tokens 188 us (1.28 PFLOP/s), 512 tokens 63 us, 128 tokens
+// 32 us, 24 tokens 20 us; 64 experts of 1536 x 2048, 2048 tokens x 8: 126 us.
 #include "ql_internal.h"
 #include "ql_w4.cuh"
 
@@ -39,7 +52,8 @@ constexpr int kG4MaxSplit = 8;
 constexpr int64_t kG4CountPairs = 2048;  // experts: up to here each pair's place is counted by its own warp
 
 // Wide kernel: two 128-row weight tiles share up to 192 tokens; one CTA to an SM, which
-// takes tile after tile.  TMEM: 2 x 192 accumulator columns, 2 slots x 2 tiles x 32.
+// takes tile after tile.  An MMA issuer to each weight tile (one for both: 2048 tokens
+// 14336 x 4096 197 against 188 us).  TMEM: 2 x 192 accumulator columns, 2 slots x 2 tiles x 32.
 constexpr int kWideTok = 192;
 constexpr int kWideRing = 110592;  // bytes of token stages
 constexpr int kWideProducer = kG4DequantWarps;
