@@ -536,6 +536,16 @@ def _on(t: torch.Tensor, dtype, name: str, device: int) -> int:
     return p
 
 
+def _out(t, shape: tuple, dtype, like: torch.Tensor, name: str, device: int):
+    """An output and its address: the caller's, checked, or a new one beside `like`."""
+    if t is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape}")
+    return t, _on(t, dtype, name, device)
+
+
 def _launch_stream(stream, device: int) -> int:
     """The stream's handle; the current one without building a Stream object
     (3.2 us of a 12 us call)."""
@@ -618,13 +628,10 @@ def forward_w4(x: torch.Tensor, w: W4Weight, workspace: torch.Tensor | None = No
     if workspace is None:
         nb = L.qlinear_forward_w4_workspace_bytes(M, w._p)
         workspace = _scratch(nb, stream) if nb else None
-    if y is None:
-        y = x.new_empty((M, w.N))
-    elif tuple(y.shape) != (M, w.N):
-        raise ValueError(f"y must be {(M, w.N)}")
+    xp = _on(x, torch.bfloat16, "x", dev)
+    y, yp = _out(y, (M, w.N), torch.bfloat16, x, "y", dev)
     wp, wn = (None, 0) if workspace is None else (_on(workspace, torch.uint8, "workspace", dev), workspace.numel())
-    _check(L.qlinear_forward_w4(_on(x, torch.bfloat16, "x", dev), w._p, M, _on(y, torch.bfloat16, "y", dev), wp, wn,
-                                _launch_stream(stream, dev)), "qlinear_forward_w4")
+    _check(L.qlinear_forward_w4(xp, w._p, M, yp, wp, wn, _launch_stream(stream, dev)), "qlinear_forward_w4")
     return y
 
 
@@ -651,7 +658,9 @@ class _RouteConfig(ctypes.Structure):
 
 @functools.lru_cache(maxsize=256)
 def _route_config(*fields) -> _RouteConfig:
-    return _RouteConfig(*fields)
+    c = _RouteConfig(*fields)
+    c.address = ctypes.addressof(c)
+    return c
 
 
 def route(logits: torch.Tensor, top_k: int, score: int = ROUTE_SOFTMAX, bias: torch.Tensor | None = None,
@@ -671,15 +680,10 @@ def route(logits: torch.Tensor, top_k: int, score: int = ROUTE_SOFTMAX, bias: to
         bp = _on(bias, torch.float32, "bias", dev)
         if bias.numel() != E:
             raise ValueError(f"bias must have {E} entries")
-    if ids is None:
-        ids = logits.new_empty((T, top_k), dtype=torch.int32)
-    if weights is None:
-        weights = logits.new_empty((T, top_k), dtype=torch.float32)
-    if tuple(ids.shape) != (T, top_k) or tuple(weights.shape) != (T, top_k):
-        raise ValueError(f"ids and weights must be {(T, top_k)}")
-    c = _route_config(E, top_k, groups, top_groups, group_top, score, bool(renormalize), scale)
-    _check(lib().qlinear_route(lp, bf16, ctypes.addressof(c), bp, T, _on(ids, torch.int32, "ids", dev),
-                               _on(weights, torch.float32, "weights", dev), _launch_stream(stream, dev)), "qlinear_route")
+    ids, ip = _out(ids, (T, top_k), torch.int32, logits, "ids", dev)
+    weights, wp = _out(weights, (T, top_k), torch.float32, logits, "weights", dev)
+    c = _route_config(E, top_k, groups, top_groups, group_top, score, renormalize, scale)
+    _check(lib().qlinear_route(lp, bf16, c.address, bp, T, ip, wp, _launch_stream(stream, dev)), "qlinear_route")
     return ids, weights
 
 
@@ -709,13 +713,10 @@ def experts_w4(x: torch.Tensor, ids: torch.Tensor, w: W4Weight, weights: torch.T
         nb = L.qlinear_experts_w4_workspace_bytes(T, k, w._p, combine)
         workspace = _scratch(nb, stream) if nb else None
     shape = (T, w.N) if combine else (T, k, w.N)
-    if y is None:
-        y = x.new_empty(shape)
-    elif tuple(y.shape) != shape:
-        raise ValueError(f"y must be {shape}")
+    xp, ip = _on(x, torch.bfloat16, "x", dev), _on(ids, torch.int32, "ids", dev)
+    y, yp = _out(y, shape, torch.bfloat16, x, "y", dev)
     wp, wn = (None, 0) if workspace is None else (_on(workspace, torch.uint8, "workspace", dev), workspace.numel())
-    _check(L.qlinear_experts_w4(_on(x, torch.bfloat16, "x", dev), _on(ids, torch.int32, "ids", dev), gp, w._p, T, k,
-                                _on(y, torch.bfloat16, "y", dev), wp, wn, _launch_stream(stream, dev)), "qlinear_experts_w4")
+    _check(L.qlinear_experts_w4(xp, ip, gp, w._p, T, k, yp, wp, wn, _launch_stream(stream, dev)), "qlinear_experts_w4")
     return y
 
 
