@@ -67,6 +67,18 @@ def test_large_experts_for_few_tokens(cuda, combine, group, zeros, T):
 
 
 @pytest.mark.parametrize("combine", [False, True])
+@pytest.mark.parametrize("T,k,E,N,K,group,zeros", [
+    (16, 32, 64, 40, 64, 32, False), (70, 32, 1024, 8, 32, 32, True), (700, 4, 24, 65, 96, 64, True),
+    (1030, 2, 1, 72, 288, 128, False), (650, 4, 40, 264, 2080, 32, False)])
+def test_many_pairs(cuda, combine, T, k, E, N, K, group, zeros):
+    """The most slots and experts; more pairs than are placed by counting; ids out of
+    range among them."""
+    x, ids, wq, sw, wz, wts = _case(T, k, E, N, K, group, zeros, combine)
+    ids[1, 0], ids[T // 2, 1], ids[-1, :] = E, -1, -5
+    _check(x, ids, wq, sw, wz, wts, group)
+
+
+@pytest.mark.parametrize("combine", [False, True])
 @pytest.mark.parametrize("T", [1, 5, 8, 13, 40])
 @pytest.mark.parametrize("kind", ["one expert", "same expert twice", "out of range", "nothing"])
 def test_uneven_ids(cuda, combine, T, kind):

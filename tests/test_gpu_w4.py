@@ -54,7 +54,8 @@ def test_product(cuda, group, zeros, M, N, K):
     (1, 1024, 4096, 128, False), (3, 4096, 14336, 128, True), (12, 14336, 4096, 64, False), (24, 4096, 4096, 32, True),
     (512, 1024, 4096, 128, False), (1, 4096, 4096, 32, True), (8, 6144, 4096, 64, True), (16, 4096, 4160, 128, True),
     (2, 5003, 4128, 128, False), (9, 14336, 992, 32, False), (300, 14336, 992, 64, True), (1030, 8197, 512, 128, False),
-    (400, 20001, 160, 32, True), (130, 4096, 4096, 64, True), (300, 1030, 4128, 32, False)])
+    (400, 20001, 160, 32, True), (130, 4096, 4096, 64, True), (300, 1030, 4128, 32, False),
+    (700, 20000, 32, 32, False), (20, 300, 32, 32, True), (900, 20008, 64, 64, True)])
 def test_product_layer_sizes(cuda, M, N, K, group, zeros):
     """Decoder layer sizes, and the same call twice in one workspace gives the same bits."""
     x, wq, sw, wz = _case(M, N, K, group, zeros)
