@@ -175,3 +175,32 @@ def test_route_up_activation_down(cuda, T):
     torch.cuda.synchronize()
     verify(out, x2, l2)
     assert ql.device_status()[0] == 0
+
+
+def test_two_streams_at_once(cuda):
+    """Calls in flight on two streams, each with its own workspace, give what they give
+    alone: every kind of tile beside every other."""
+    x, ids, wq, sw, wz, wts = _case(300, 4, 6, 520, 1056, 64, True, True)
+    experts = ql.W4Weight(wq.cuda(), sw.cuda(), wz.cuda(), 64)
+    g = _gen(11)
+    dense = ql.W4Weight(*(t.cuda() for t in _w4.make_weights(g, (4096,), 2048, 128, True)), 128)
+    xs = [torch.randn(M, 2048, generator=g).bfloat16().cuda() for M in (1, 16, 40, 128, 700)]
+    xd, idd, wd = x.cuda(), ids.cuda(), wts.cuda()
+    calls = [lambda ws, v=v: ql.forward_w4(v, dense, workspace=ws) for v in xs]
+    calls += [lambda ws, T=T: ql.experts_w4(xd[:T], idd[:T], experts, weights=wd[:T], workspace=ws) for T in (5, 60, 300)]
+    size = max([ql.forward_w4_workspace_bytes(len(v), dense) for v in xs] +
+               [ql.experts_w4_workspace_bytes(300, 4, experts, combine=True)])
+    alone = [c(None) for c in calls]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [ql.new_workspace(size) for _ in streams]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for i in range(2 * len(calls)):
+        for n, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[n].append(calls[(i + 3 * n) % len(calls)](spaces[n]))
+    torch.cuda.synchronize()
+    assert ql.device_status()[0] == 0
+    for n in range(2):
+        for i, y in enumerate(got[n]):
+            assert torch.equal(y, alone[(i + 3 * n) % len(calls)]), (n, i)
