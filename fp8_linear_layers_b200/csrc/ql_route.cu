@@ -135,7 +135,11 @@ __device__ __noinline__ void select_f64(const RouteParams& p, const void* row, f
     uint32_t kept = kFull;
     if (pass == 1 && p.G > 1) kept = (uint32_t)my_id;
     __syncwarp();
-    for (int e = lane; e < p.E; e += 32) {
+    const bool again = pass == 1 && p.G > 1 && (p.bias || p.group_top == 1);  // the groups' pass made these values
+    for (int e = lane; again && e < p.E; e += 32)
+      if (!((kept >> (((e * p.gmagic) >> 20) & 31)) & 1u)) c[e] = kNone;
+#pragma unroll 4
+    for (int e = lane; !again && e < p.E; e += 32) {
       const float l = load_logit<kBf16>(row, e);
       double v = kNone;
       if (usable(l)) {
