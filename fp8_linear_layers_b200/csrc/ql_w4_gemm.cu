@@ -509,6 +509,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
 struct WideTile {
   int64_t e, m0;  // expert; first token row
   int count, rt, tt;
+  unsigned by;    // experts: the expert; dense: the token tile
+  // The first of n weight stages (G4Range): by the expert and not by the token tile, since
+  // which of its expert's tiles a pair stands in may depend on timing (w4_plan_kernel), and
+  // the order of a sum must not.
+  QL_DEVINL int rot(int n) const { return (int)((rt * 5 + by * 3) % (unsigned)n); }
 };
 
 template <bool kExperts>
@@ -521,8 +526,10 @@ QL_DEVINL WideTile wide_tile(const G4Params& p, int t) {
     w.e = g.expert;
     w.m0 = g.start;
     w.count = g.count;
+    w.by = (unsigned)g.expert;
   } else {
     w.e = 0;
+    w.by = (unsigned)w.tt;
     w.m0 = (int64_t)w.tt * p.ntok;
     w.count = (int)min((int64_t)p.ntok, p.M - w.m0);
   }
@@ -617,7 +624,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     uint32_t fill = 0;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const WideTile w = wide_tile<kExperts>(p, t);
-      kr.rot = (w.rt * 5 + w.tt * 3) % kr.n;
+      kr.rot = w.rot(kr.n);
       const int wrow = (int)(w.e * p.N + (int64_t)w.rt * 256);
       for (int j = 0; j < kr.n && ok; ++j) {
         const int v = jw % kG4WStages, ws = kr.stage(j);
@@ -704,7 +711,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     int g = 0, jw = 0, it = 0;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++it) {
       const WideTile w = wide_tile<kExperts>(p, t);
-      kr.rot = (w.rt * 5 + w.tt * 3) % kr.n;
+      kr.rot = w.rot(kr.n);
       const int64_t wr = w.e * p.N + min((int64_t)w.rt * 256 + row, p.N - 1);
       const uint16_t* sw = p.sw + wr * p.groups;
       const uint8_t* wz = kZero ? p.wz + wr * p.groups : nullptr;
@@ -928,7 +935,7 @@ QL_DEVINL int plan_tiles(const G4PrepParams& p, int* hist) {
 
 // Many pairs: one block plans and gives every pair its place.  The order inside an
 // expert depends on timing; results do not, since a pair is one MMA column wherever it
-// stands.
+// stands, and all of an expert's tiles take K in the same order (WideTile::rot).
 __global__ void __launch_bounds__(kG4PlanThreads) w4_plan_kernel(const G4PrepParams p) {
   __shared__ int hist[kG4PlanThreads];
   tc::grid_dependency_wait();
