@@ -63,7 +63,9 @@ constexpr int kWideEpiWarps = 8;
 constexpr int kWideThreads = (kWideFirstEpi + kWideEpiWarps) * 32;
 constexpr int kWideBarriers = 2 * kG4WStages + 2 * kG4MaxXStages + 12;
 constexpr int kWideStageRow = 80;  // bytes of a token in an epilogue warp's staging (32 outputs and a pad)
+constexpr int kWideStageRowF32 = 144;  // the same of f32 outputs, 8 tokens at a time
 constexpr int kWideWBytes = 2 * 128 * 128;
+static_assert(8 * kWideStageRowF32 <= 16 * kWideStageRow, "staging");
 
 // Narrow kernel: one weight tile, up to 128 tokens, K split over a cluster; two CTAs to
 // an SM.  TMEM: 128 accumulator columns, 4 slots x 32.
@@ -80,7 +82,8 @@ struct G4Tile {
 struct G4Params {
   const uint16_t* sw;
   const uint8_t* wz;
-  uint16_t* y;           // dense, gather: the result; combine: the pairs' products
+  uint16_t* y;           // dense, gather: the result
+  float* yp;             // combine: the pairs' products; else null
   const int* ex;         // exponents of the prepared tokens (experts: of the sorted pairs)
   const int* order;      // experts: pairs sorted by expert
   const G4Tile* tiles;   // experts: token tiles
@@ -811,7 +814,29 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = scale2(__uint_as_float(v[i]), -(f + (c + i < w.count ? s_ex[buf + c + i] : 0)));
         }
-        if (vec) {
+        if (kExperts && p.yp) {  // f32: half the tokens at a time fit the staging
+#pragma unroll
+          for (int h = 0; h < 16; h += 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<float*>(stg + i * kWideStageRowF32 + lane * 4) = o[h + i];
+            __syncwarp();
+            if (p.N & 3) {
+              for (int i = 0; i < 8; ++i)
+                if (c + h + i < w.count && nw + lane < p.N)
+                  p.yp[s_out[buf + c + h + i] * p.N + nw + lane] =
+                      *reinterpret_cast<const float*>(stg + i * kWideStageRowF32 + lane * 4);
+            } else if (nw + (lane & 7) * 4 < p.N) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int row = i * 4 + (lane >> 3), tok = c + h + row;
+                if (tok < w.count)
+                  *reinterpret_cast<float4*>(p.yp + s_out[buf + tok] * p.N + nw + (lane & 7) * 4) =
+                      *reinterpret_cast<const float4*>(stg + row * kWideStageRowF32 + (lane & 7) * 16);
+              }
+            }
+            __syncwarp();
+          }
+        } else if (vec) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             *reinterpret_cast<uint16_t*>(stg + i * kWideStageRow + lane * 2) = f32_to_bf16_rn(o[i]);
@@ -1112,11 +1137,11 @@ __global__ void __launch_bounds__(kG4PlanThreads) w4_prepare_pairs_kernel(const 
   x.each([&](const uint4& v, int i) { dst[i] = prepare8(v, f0, f1); });
 }
 
-// y[t] = sum_j weights[t, j] yp[t, j], the pairs' products rounded to bf16 (half the
-// traffic of f32 between the two kernels; one more rounding of each term).  A thread
+// y[t] = sum_j weights[t, j] yp[t, j] in the order of j, all in f32: the terms of a token may
+// cancel, so a rounded term could be off by more than the whole result's rounding.  A thread
 // takes kVec neighbouring outputs; bound by the pairs' bytes.
 template <int kVec>
-__global__ void __launch_bounds__(256) w4_combine_kernel(const uint16_t* __restrict__ yp, const int32_t* __restrict__ ids,
+__global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict__ yp, const int32_t* __restrict__ ids,
                                                          const float* __restrict__ weights, int topk, int E, int64_t N,
                                                          int64_t T, uint16_t* __restrict__ y) {
   tc::grid_dependency_wait();
@@ -1131,33 +1156,33 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(const uint16_t* __restr
   for (int j0 = 0; j0 < topk; j0 += kAhead) {
     float w[kAhead];
     bool use[kAhead];
-    uint4 v[kAhead];
+    float4 v[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int e = j0 + j < topk ? __ldg(ids + t * topk + j0 + j) : -1;
       use[j] = e >= 0 && e < E;
       w[j] = use[j] ? __ldg(weights + t * topk + j0 + j) : 0.0f;
       if (!use[j]) continue;  // (not a product with zero: the place holds anything)
-      const uint16_t* src = yp + (t * topk + j0 + j) * N + n;
-      if constexpr (kVec == 8)
-        v[j] = *reinterpret_cast<const uint4*>(src);
+      const float* src = yp + (t * topk + j0 + j) * N + n;
+      if constexpr (kVec == 4)
+        v[j] = *reinterpret_cast<const float4*>(src);
       else
         v[j].x = *src;
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (!use[j]) continue;
-      const uint32_t q[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) sum[i] = fmaf(w[j], i % 2 ? bf16_hi(q[i / 2]) : bf16_lo(q[i / 2]), sum[i]);
+      sum[0] = fmaf(w[j], v[j].x, sum[0]);
+      if constexpr (kVec == 4) {
+        sum[1] = fmaf(w[j], v[j].y, sum[1]);
+        sum[2] = fmaf(w[j], v[j].z, sum[2]);
+        sum[3] = fmaf(w[j], v[j].w, sum[3]);
+      }
     }
   }
-  if constexpr (kVec == 8) {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = (uint32_t)f32_to_bf16_rn(sum[2 * i]) | (uint32_t)f32_to_bf16_rn(sum[2 * i + 1]) << 16;
-    *reinterpret_cast<uint4*>(y + t * N + n) = make_uint4(o[0], o[1], o[2], o[3]);
+  if constexpr (kVec == 4) {
+    *reinterpret_cast<uint2*>(y + t * N + n) =
+        make_uint2(w4::f32x2_to_bf16x2(sum[0], sum[1]), w4::f32x2_to_bf16x2(sum[2], sum[3]));
   } else {
     y[t * N + n] = f32_to_bf16_rn(sum[0]);
   }
@@ -1262,7 +1287,7 @@ G4Layout g4_layout(int64_t rows, int64_t K, int64_t pairs, unsigned tiles, int64
   L.ntiles = off;
   off += 256;
   L.yp = off;
-  off += up256((size_t)yp_elems * 2);
+  off += up256((size_t)yp_elems * 4);
   L.total = off;
   return L;
 }
@@ -1426,9 +1451,9 @@ cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float
                 : launch_pdl(w4_prepare_experts_kernel, (unsigned)T + 1, kG4PlanThreads, q, st);
   }
   if (e != cudaSuccess) return e;
-  uint16_t* yp = combine ? reinterpret_cast<uint16_t*>(ws + L.yp) : y;
   G4Params p = {};
-  p.y = yp;
+  p.y = y;
+  p.yp = combine ? reinterpret_cast<float*>(ws + L.yp) : nullptr;
   p.ex = q.ex;
   p.order = q.order;
   p.tiles = q.tiles;
@@ -1437,7 +1462,7 @@ cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float
   e = launch_g4<true>(w, q.x16, pairs, p, g, sms, st);
   if (e != cudaSuccess || !combine) return e;
   cudaLaunchConfig_t cfg = {};
-  const int64_t threads = w.N % 8 ? T * w.N : T * (w.N / 8);
+  const int64_t threads = w.N % 4 ? T * w.N : T * (w.N / 4);
   if (div_up(threads, 256) >= (int64_t(1) << 31)) return cudaErrorNotSupported;
   cfg.gridDim = dim3((unsigned)div_up(threads, 256));
   cfg.blockDim = dim3(256);
@@ -1447,7 +1472,7 @@ cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, w.N % 8 ? w4_combine_kernel<1> : w4_combine_kernel<8>, (const uint16_t*)yp, ids,
+  return cudaLaunchKernelEx(&cfg, w.N % 4 ? w4_combine_kernel<1> : w4_combine_kernel<4>, (const float*)p.yp, ids,
                             weights, (int)topk, (int)w.experts, w.N, T, y);
 }
 
