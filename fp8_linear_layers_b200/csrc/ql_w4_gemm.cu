@@ -9,14 +9,18 @@
 // column = two inputs, so no swizzled shared-memory store is needed and the shared
 // memory serves only the tokens' operand.
 //
-// f16 carries both operands without loss.  A scaled weight (q - z) s has at most 3 + 8
-// significant bits for z = 8 and 4 + 8 with zero points, f16 has 11; x is bf16, 8
-// bits.  Their exponents are brought into f16's range by powers of two: each token is
-// scaled so that its largest |x| lies in [2^14, 2^15) (values more than 2^31 below it
-// lose bits), each weight row so that its largest |s| lies in [2^10, 2^11).  Sums are
-// f32, and the powers of two come off in the epilogue.  Scaling in f16 before the
-// product leaves nothing to do at a group's end, so 32-input groups cost what
-// 128-input groups do.
+// f16 has 11 significant bits.  x is bf16, 8 bits, and fits; so does a scaled weight
+// (q - 8) s, 3 + 8 bits.  With zero points (q - z) s may need 4 + 8: it is rounded once to
+// 11, off by at most 2^-11 of itself.  That is a choice: the two halves of a 12-bit weight
+// would take two MMAs, twice the tensor time, for an eighth of what bf16 weights lose.
+// Exponents are brought into f16's range by powers of two: each token is scaled so that its
+// largest |x| lies in [2^14, 2^15), each weight row so that its largest |s| lies in [2^10,
+// 2^11).  Inputs more than 2^31 below their token's largest and scales more than 2^27 below
+// their row's do not fit; they are zero for the tensor cores, and the epilogue adds their
+// products (left_out: of tokens of 4096 N(0, 1) inputs with outliers 20 times larger about one
+// in 10,000 has such an input; a tile with all of them, K = 16384, takes 0.2 s).  Sums are f32,
+// and the powers of two come off in the epilogue.  Scaling in f16 before the product leaves
+// nothing to do at a group's end, so 32-input groups cost what 128-input groups do.
 //
 // A prepare kernel makes the f16 tokens (the inputs of each eight in the order 0 4 1 5
 // 2 6 3 7 in which codes_to_f16 gives the weights) and, for experts, sorts the (token,
@@ -80,12 +84,15 @@ struct G4Tile {
 };
 
 struct G4Params {
+  const uint16_t* x;     // the tokens as given (left_out)
+  const uint8_t* wq;
   const uint16_t* sw;
   const uint8_t* wz;
   uint16_t* y;           // dense, gather: the result
   float* yp;             // combine: the pairs' products; else null
-  const int* ex;         // exponents of the prepared tokens (experts: of the sorted pairs)
+  const int* ex;         // G4Row::exponent of the prepared tokens (experts: of the sorted pairs)
   const int* order;      // experts: pairs sorted by expert
+  int slots;             // experts: pairs of an x row
   const G4Tile* tiles;   // experts: token tiles
   const int* ntiles;
   int64_t N, K;
@@ -112,23 +119,121 @@ QL_DEVINL int log2_bf16(uint32_t mag, int zero) {
   return mag >= 0x80u ? (int)(mag >> 7) - 127 : mag ? -133 + (31 - __clz(mag)) : zero;
 }
 
-// The power of two f that brings a row's largest |s| over groups [g0, g1) to [2^10, 2^11).
+// A value whose scaled magnitude is below 2^-17 may not fit f16 (8 significant bits down to
+// 2^-24): it is "left out", zero for the tensor cores, and its products are added by the
+// epilogue (left_out).  The bf16 magnitude from which on a value scaled by 2^e stays in.
+QL_DEVINL uint32_t left_out_below(int e) {
+  const int t = -17 - e;  // in [-164, 100]
+  return t >= -126 ? (uint32_t)(t + 127) << 7 : t >= -133 ? 1u << (t + 133) : 0u;
+}
+// low: the smallest nonzero magnitude less one.
+QL_DEVINL bool leaves_out(uint32_t low, int e) {
+  const uint32_t thr = left_out_below(e);
+  return low < thr && low + 1u < thr;
+}
+
+// 2 f + 1 if scales are left out, else 2 f: f the power of two that brings a row's largest
+// |s| over groups [g0, g1) to [2^10, 2^11).
 QL_DEVINL int row_exponent(const uint16_t* sw, int g0, int g1, bool vec) {
-  uint32_t top = 0;
+  uint32_t top = 0, low = 0xFFFFFFFFu;
+  auto add = [&](uint32_t mag) {
+    top = max(top, mag);
+    low = min(low, mag - 1u);
+  };
   if (vec) {  // whole 16-byte pieces; a neighbour's scales do no harm beyond range
     const uint4* v4 = reinterpret_cast<const uint4*>(sw);
 #pragma unroll 4
     for (int i = g0 >> 3; i < (g1 + 7) >> 3; ++i) {
       const uint4 v = __ldg(v4 + i);
-      top = max(max(max(top, v.x & 0x7FFFu), max(v.x >> 16 & 0x7FFFu, v.y & 0x7FFFu)),
-                max(max(v.y >> 16 & 0x7FFFu, v.z & 0x7FFFu),
-                    max(v.z >> 16 & 0x7FFFu, max(v.w & 0x7FFFu, v.w >> 16 & 0x7FFFu))));
+      add(v.x & 0x7FFFu), add(v.x >> 16 & 0x7FFFu);
+      add(v.y & 0x7FFFu), add(v.y >> 16 & 0x7FFFu);
+      add(v.z & 0x7FFFu), add(v.z >> 16 & 0x7FFFu);
+      add(v.w & 0x7FFFu), add(v.w >> 16 & 0x7FFFu);
     }
   } else {
 #pragma unroll 8
-    for (int i = g0; i < g1; ++i) top = max(top, (uint32_t)__ldg(sw + i) & 0x7FFFu);
+    for (int i = g0; i < g1; ++i) add((uint32_t)__ldg(sw + i) & 0x7FFFu);
   }
-  return 10 - log2_bf16(min(top, 0x7F7Fu), 10);
+  const int f = 10 - log2_bf16(min(top, 0x7F7Fu), 10);
+  return 2 * f + leaves_out(low, f);
+}
+
+template <class T>
+QL_DEVINL const T* shfl_pointer(const T* p, int lane) {
+  return reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), lane));
+}
+
+// What the tensor cores left out of one token's product with each lane's weight row, over
+// inputs [k0, k1): the token's values below its threshold, and the groups whose scales are
+// below their row's, in f32 from the original operands.  For a whole warp; x and ex are the
+// same in all lanes.  ex and f as G4Row::exponent and row_exponent give them.  Rare (a value
+// 2^31 below its token's largest, a scale 2^27 below its row's), so a walk over the token
+// will do.
+template <int kGroup, bool kZero>
+__device__ __noinline__ float left_out(const uint16_t* x, const uint8_t* wq, const uint16_t* sw, const uint8_t* wz,
+                                       int ex, int f, int k0, int k1) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t xthr = left_out_below(ex >> 1);
+  float sum = 0.0f;
+  if (ex & 1) {
+    for (int base = k0; base < k1; base += 256) {
+      const int k = base + lane * 8;
+      uint32_t v[4] = {0, 0, 0, 0};
+      if (k < k1) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + k));
+        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // the nonzero values below the threshold, else 0
+          v[i] = ((v[i] & 0x7FFFu) - 1u < xthr - 1u ? v[i] & 0xFFFFu : 0u) |
+                 ((v[i] >> 16 & 0x7FFFu) - 1u < xthr - 1u ? v[i] & 0xFFFF0000u : 0u);
+      }
+      unsigned pieces = __ballot_sync(0xffffffffu, (v[0] | v[1] | v[2] | v[3]) != 0);
+      while (pieces) {
+        const int src = __ffs(pieces) - 1, kk = base + src * 8, g = kk / kGroup;
+        pieces &= pieces - 1;
+        const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(wq + (kk >> 1)));
+        const float s = __uint_as_float((uint32_t)__ldg(sw + g) << 16);
+        const int z = kZero ? __ldg(wz + g) : 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t u = __shfl_sync(0xffffffffu, v[i], src);
+          const int q0 = (int)(c >> (8 * i) & 15u) - z, q1 = (int)(c >> (8 * i + 4) & 15u) - z;
+          if (u & 0xFFFFu) sum = fmaf(bf16_lo(u) * (float)q0, s, sum);
+          if (u >> 16) sum = fmaf(bf16_hi(u) * (float)q1, s, sum);
+        }
+      }
+    }
+  }
+  unsigned rows = __ballot_sync(0xffffffffu, f & 1);
+  while (rows) {
+    const int r = __ffs(rows) - 1;
+    rows &= rows - 1;
+    const uint32_t sthr = left_out_below(__shfl_sync(0xffffffffu, f, r) >> 1);
+    const uint8_t* rw = shfl_pointer(wq, r);
+    const uint16_t* rs = shfl_pointer(sw, r);
+    const uint8_t* rz = shfl_pointer(wz, r);
+    float part = 0.0f;
+#pragma unroll 4
+    for (int k = k0 + lane * 8; k < k1; k += 256) {
+      const uint32_t s16 = __ldg(rs + k / kGroup);
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + k));
+      const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(rw + (k >> 1))), v[4] = {u.x, u.y, u.z, u.w};
+      const int z = kZero ? __ldg(rz + k / kGroup) : 8;
+      const float s = __uint_as_float(s16 << 16);
+      const bool out = (s16 & 0x7FFFu) - 1u < sthr - 1u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // (the token's own were added above)
+        const int q0 = (int)(c >> (8 * i) & 15u) - z, q1 = (int)(c >> (8 * i + 4) & 15u) - z;
+        if (out && (v[i] & 0x7FFFu) >= xthr) part = fmaf(bf16_lo(v[i]), (float)q0 * s, part);
+        if (out && (v[i] >> 16 & 0x7FFFu) >= xthr) part = fmaf(bf16_hi(v[i]), (float)q1 * s, part);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == r) sum += part;
+  }
+  return sum;
 }
 
 // A row's scales and zero points of a weight stage's granules kStep i + first, loaded a
@@ -150,10 +255,10 @@ struct G4Scales {
       if constexpr (kZero) zraw[i] = gi < groups ? __ldg(wz + gi) : 8;
     }
   }
-  QL_DEVINL void convert(int f) {
+  QL_DEVINL void convert(int f, uint32_t below) {  // below: left_out_below(f)
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const float s = scale2(__uint_as_float(sraw[i] << 16), f);
+      const float s = (sraw[i] & 0x7FFFu) < below ? 0.0f : scale2(__uint_as_float(sraw[i] << 16), f);
       s2[i] = w4::f32x2_to_f16x2(s, s);
       if constexpr (kZero) {
         z0[i] = 0x64006400u + zraw[i] * 0x10001u;
@@ -221,7 +326,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   float* s_fac = reinterpret_cast<float*>(s_ex + kNarrowTok); // 2^-exponent
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_fac + kNarrowTok);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* s_wide = reinterpret_cast<int*>(tmem_holder + 2);  // an exponent that one factor cannot take
+  int* s_wide = reinterpret_cast<int*>(tmem_holder + 2);  // an exponent that one factor cannot take, or values left out
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % p.splits;
@@ -265,10 +370,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   const int64_t m0 = (int64_t)blockIdx.y * p.ntok;
   const int count = (int)min((int64_t)p.ntok, p.M - m0);
   for (int i = threadIdx.x; i < count; i += kThreads) {
-    const int ex = p.ex[m0 + i];
+    const int ex = p.ex[m0 + i], e = ex >> 1;
     s_ex[i] = ex;
-    s_fac[i] = exp2i(max(-126, min(126, -ex)));
-    if (abs(ex) > 60) *s_wide = 1;
+    s_fac[i] = exp2i(max(-126, min(126, -e)));
+    if (abs(e) > 60 || (ex & 1)) *s_wide = 1;
   }
   tc::fence_before();
   __syncthreads();
@@ -361,7 +466,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     const uint16_t* sw = p.sw + wr * p.groups;
     const uint8_t* wz = kZero ? p.wz + wr * p.groups : nullptr;
     G4Scales<kGroup, kZero, 2> sc;
-    const int f = row_exponent(sw, kr.w0 * sc.kStage, min(p.groups, (kr.w0 + kr.n) * sc.kStage), (p.groups & 7) == 0);
+    const int fl = row_exponent(sw, kr.w0 * sc.kStage, min(p.groups, (kr.w0 + kr.n) * sc.kStage), (p.groups & 7) == 0);
+    const int f = fl >> 1;
+    const uint32_t below = left_out_below(f);
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
     const uint32_t row_off = (uint32_t)((q * 32 + lane) * 128);
     sc.load(sw, wz, kr.stage(0), wg, p.groups);
@@ -369,7 +476,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     int j0 = 0;  // the stage's first granule
     for (int jw = 0; jw < kr.n && ok; ++jw) {
       const int ws = jw % kG4WStages, ng = kr.granules(kr.stage(jw));
-      sc.convert(f);
+      sc.convert(f, below);
       if (jw + 1 < kr.n) sc.load(sw, wz, kr.stage(jw + 1), wg, p.groups);
       ok = w4::wait(&wfull[ws], (jw / kG4WStages) & 1, abort_flag);
       if (!ok) break;
@@ -413,7 +520,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
       const int col = q * 32 + lane;
       const int half = ((mma_n / 16 + 1) / 2) * 16;
       const int c_lo = wg ? half : 0, c_hi = wg ? mma_n : half;
-      const bool wide = __any_sync(0xffffffffu, *s_wide || abs(f) > 60);
+      const bool rows_out = __any_sync(0xffffffffu, fl & 1);
+      const bool wide = __any_sync(0xffffffffu, *s_wide || abs(f) > 60) || rows_out;
       const float rf = exp2i(max(-126, min(126, -f)));
       for (int c = c_lo; c < c_hi; c += 16) {
         float o[16];
@@ -425,7 +533,18 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
           for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(v[i]) * rf * s_fac[c + i];
         } else {  // the two factors may leave f32's range where their product does not
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = scale2(__uint_as_float(v[i]), -(f + (c + i < count ? s_ex[c + i] : 0)));
+          for (int i = 0; i < 16; ++i)
+            o[i] = scale2(__uint_as_float(v[i]), -(f + (c + i < count ? s_ex[c + i] >> 1 : 0)));
+#pragma unroll 1
+          for (int i = 0; i < min(16, count - c); ++i) {
+            const int ex = s_ex[c + i];
+            if (!(ex & 1) && !rows_out) continue;
+            const float more = left_out<kGroup, kZero>(p.x + (m0 + c + i) * p.K, p.wq + wr * (p.K >> 1), sw, wz, ex, fl,
+                                                       kr.w0 * kG4StageK, min((int)p.K, (kr.w0 + kr.n) * kG4StageK));
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (j == i) o[j] += more;
+          }
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -720,11 +839,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const uint8_t* wz = kZero ? p.wz + wr * p.groups : nullptr;
       G4Scales<kGroup, kZero, 1> sc;
       sc.load(sw, wz, kr.stage(0), 0, p.groups);
-      const int f = row_exponent(sw, 0, p.groups, (p.groups & 7) == 0);
-      s_f[(it & 3) * 256 + row] = f;
+      const int fl = row_exponent(sw, 0, p.groups, (p.groups & 7) == 0), f = fl >> 1;
+      const uint32_t below = left_out_below(f);
+      s_f[(it & 3) * 256 + row] = fl;
       for (int j = 0; j < kr.n && ok; ++j, ++jw) {
         const int ws = jw % kG4WStages, ng = kr.granules(kr.stage(j));
-        sc.convert(f);
+        sc.convert(f, below);
         if (j + 1 < kr.n) sc.load(sw, wz, kr.stage(j + 1), 0, p.groups);
         ok = w4::wait(&wfull[ws], (jw / kG4WStages) & 1, abort_flag);
         if (!ok) break;
@@ -775,16 +895,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int ex = p.ex[w.m0 + et];
         if constexpr (kExperts) s_out[buf + et] = p.order[w.m0 + et];
         s_ex[buf + et] = ex;
-        s_fac[buf + et] = exp2i(max(-126, min(126, -ex)));
-        wide = abs(ex) > 60;
+        s_fac[buf + et] = exp2i(max(-126, min(126, -(ex >> 1))));
+        wide = abs(ex >> 1) > 60 || (ex & 1);
       }
-      wide = wide_epi_any(wide);  // an exponent that one factor cannot take
+      wide = wide_epi_any(wide);  // an exponent that one factor cannot take, or values left out
       ok = w4::wait(&dfull[r], it & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok && !*abort_flag);
       if (wide_epi_any(!ok)) break;
       tc::fence_after();
-      const int f = s_f[(it & 3) * 256 + r * 128 + q * 32 + lane];
-      wide = __any_sync(0xffffffffu, wide || abs(f) > 60);
+      const int fl = s_f[(it & 3) * 256 + r * 128 + q * 32 + lane], f = fl >> 1;
+      const bool rows_out = __any_sync(0xffffffffu, fl & 1);
+      wide = __any_sync(0xffffffffu, wide || abs(f) > 60) || rows_out;
       const float rf = exp2i(max(-126, min(126, -f)));
       const int64_t nw = (int64_t)w.rt * 256 + r * 128 + q * 32;  // the warp's first output
       uint16_t* yb = p.y + nw + (lane & 3) * 8;                    // this lane's piece of an output row
@@ -812,7 +933,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
         } else {  // the two factors may leave f32's range where their product does not
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = scale2(__uint_as_float(v[i]), -(f + (c + i < w.count ? s_ex[buf + c + i] : 0)));
+          for (int i = 0; i < 16; ++i)
+            o[i] = scale2(__uint_as_float(v[i]), -(f + (c + i < w.count ? s_ex[buf + c + i] >> 1 : 0)));
+#pragma unroll 1
+          for (int i = 0; i < min(16, w.count - c); ++i) {
+            const int ex = s_ex[buf + c + i];
+            if (!(ex & 1) && !rows_out) continue;
+            const int64_t wr = w.e * p.N + min(nw + lane, p.N - 1);
+            const int64_t xr = kExperts ? s_out[buf + c + i] / p.slots : w.m0 + c + i;
+            const float more = left_out<kGroup, kZero>(p.x + xr * p.K, p.wq + wr * (p.K >> 1), p.sw + wr * p.groups,
+                                                       kZero ? p.wz + wr * p.groups : nullptr, ex, fl, 0, (int)p.K);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (j == i) o[j] += more;
+          }
         }
         if (kExperts && p.yp) {  // f32: half the tokens at a time fit the staging
 #pragma unroll
@@ -972,17 +1106,20 @@ __global__ void __launch_bounds__(kG4PlanThreads) w4_plan_kernel(const G4PrepPar
   each_id(p, [&](int64_t i, int e) { p.pos[i] = e >= 0 ? atomicAdd(&hist[e], 1) : -1; });
 }
 
-// The largest finite magnitude of eight inputs and `top`.
-QL_DEVINL uint32_t largest8(const uint4& v, uint32_t top) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// The largest finite magnitude, and the smallest nonzero one less one.
+struct G4Span {
+  uint32_t top = 0, low = 0xFFFFFFFFu;
+  QL_DEVINL void add(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t a = w[j] & 0x7FFFu, b = w[j] >> 16 & 0x7FFFu;
-    if (a < 0x7F80u) top = max(top, a);
-    if (b < 0x7F80u) top = max(top, b);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a = w[j] & 0x7FFFu, b = w[j] >> 16 & 0x7FFFu;
+      if (a < 0x7F80u) top = max(top, a);
+      if (b < 0x7F80u) top = max(top, b);
+      low = min(low, min(a - 1u, b - 1u));
+    }
   }
-  return top;
-}
+};
 
 // A row of x for the threads of a warp (kBlock false) or of a block, held in registers
 // (kHold pieces a thread) from the search for its largest value to its conversion; a
@@ -1004,20 +1141,22 @@ struct G4Row {
       if (first + i * step < chunks) v[i] = __ldg(src + first + i * step);
     }
   }
-  // The power of two that brings the row's largest finite |x| to [2^14, 2^15).
-  QL_DEVINL int exponent(uint32_t* red) const {
-    uint32_t top = 0;
+  // 2 e + 1 if values are left out, else 2 e: e the power of two that brings the row's largest
+  // finite |x| to [2^14, 2^15).
+  QL_DEVINL int exponent(uint32_t (*red)[2]) const {
+    G4Span a;
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) top = largest8(v[i], top);
-    for (int i = first + kHold * step; i < chunks; i += step) top = largest8(__ldg(src + i), top);
-    top = __reduce_max_sync(0xffffffffu, top);
+    for (int i = 0; i < kHold; ++i) a.add(v[i]);
+    for (int i = first + kHold * step; i < chunks; i += step) a.add(__ldg(src + i));
+    a.top = __reduce_max_sync(0xffffffffu, a.top);
+    a.low = __reduce_min_sync(0xffffffffu, a.low);
     if constexpr (kBlock) {
-      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5][0] = a.top, red[threadIdx.x >> 5][1] = a.low;
       __syncthreads();
-      top = 0;
-      for (int i = 0; i < (int)blockDim.x / 32; ++i) top = max(top, red[i]);
+      for (int i = 0; i < (int)blockDim.x / 32; ++i) a.top = max(a.top, red[i][0]), a.low = min(a.low, red[i][1]);
     }
-    return 14 - log2_bf16(top, 14);
+    const int e = 14 - log2_bf16(a.top, 14);
+    return 2 * e + leaves_out(a.low, e);
   }
   // store(piece, its number) for this thread's pieces.
   template <class Store>
@@ -1029,30 +1168,44 @@ struct G4Row {
   }
 };
 
-// Eight inputs scaled by f0 f1, in the order 0 4 1 5 2 6 3 7.
-QL_DEVINL uint4 prepare8(const uint4& v, float f0, float f1) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float x[8];
+// Scales eight inputs by a token's 2^e, in the order 0 4 1 5 2 6 3 7.
+struct G4Scaler {
+  float f0, f1;
+  uint32_t below;  // magnitudes that are left out: 0 where none is
+
+  QL_DEVINL explicit G4Scaler(int ex)
+      : f0(exp2i((ex >> 1) / 2)), f1(exp2i((ex >> 1) - (ex >> 1) / 2)), below(ex & 1 ? left_out_below(ex >> 1) : 0u) {}
+  QL_DEVINL uint4 operator()(const uint4& v) const {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (below) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[2 * j] = bf16_lo(w[j]) * f0 * f1;
-    x[2 * j + 1] = bf16_hi(w[j]) * f0 * f1;
+      for (int j = 0; j < 4; ++j) {
+        if ((w[j] & 0x7FFFu) < below) w[j] &= 0xFFFF0000u;
+        if ((w[j] >> 16 & 0x7FFFu) < below) w[j] &= 0xFFFFu;
+      }
+    }
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = bf16_lo(w[j]) * f0 * f1;
+      x[2 * j + 1] = bf16_hi(w[j]) * f0 * f1;
+    }
+    return make_uint4(w4::f32x2_to_f16x2(x[0], x[4]), w4::f32x2_to_f16x2(x[1], x[5]),
+                      w4::f32x2_to_f16x2(x[2], x[6]), w4::f32x2_to_f16x2(x[3], x[7]));
   }
-  return make_uint4(w4::f32x2_to_f16x2(x[0], x[4]), w4::f32x2_to_f16x2(x[1], x[5]),
-                    w4::f32x2_to_f16x2(x[2], x[6]), w4::f32x2_to_f16x2(x[3], x[7]));
-}
+};
 
 __global__ void __launch_bounds__(kG4PrepThreads) w4_prepare_kernel(const G4PrepParams p) {
-  __shared__ uint32_t red[32];
+  __shared__ uint32_t red[32][2];
   tc::grid_dependency_wait();
   tc::launch_dependents();
   const int64_t row = blockIdx.x;
   const G4Row<true, 4> x(p.x + row * p.K, p.K);
   const int e = x.exponent(red);
   if (threadIdx.x == 0) p.ex[row] = e;
-  const float f0 = exp2i(e / 2), f1 = exp2i(e - e / 2);
+  const G4Scaler scaled(e);
   uint4* dst = reinterpret_cast<uint4*>(p.x16 + row * p.K);
-  x.each([&](const uint4& v, int i) { dst[i] = prepare8(v, f0, f1); });
+  x.each([&](const uint4& v, int i) { dst[i] = scaled(v); });
 }
 
 // A pair's place in expert order (-1: no expert), counted by its warp.
@@ -1075,7 +1228,7 @@ QL_DEVINL int count_place(const G4PrepParams& p, int pair) {
 // warp counts its pair's place itself, and block 0 plans the tiles beside the others.
 __global__ void __launch_bounds__(kG4PlanThreads) w4_prepare_experts_kernel(const G4PrepParams p) {
   __shared__ int hist[kG4PlanThreads];
-  __shared__ uint32_t red[32];
+  __shared__ uint32_t red[32][2];
   __shared__ int s_pos[32];
   tc::grid_dependency_wait();
   tc::launch_dependents();
@@ -1095,13 +1248,13 @@ __global__ void __launch_bounds__(kG4PlanThreads) w4_prepare_experts_kernel(cons
   }
   const G4Row<true, 1> x(p.x + row * p.K, p.K);
   const int e = x.exponent(red);  // (and a barrier behind s_pos)
-  const float f0 = exp2i(e / 2), f1 = exp2i(e - e / 2);
+  const G4Scaler scaled(e);
   if (threadIdx.x < p.slots && s_pos[threadIdx.x] >= 0) {
     p.ex[s_pos[threadIdx.x]] = e;
     p.order[s_pos[threadIdx.x]] = (int)row * p.slots + threadIdx.x;
   }
   x.each([&](const uint4& v, int i) {
-    const uint4 h = prepare8(v, f0, f1);
+    const uint4 h = scaled(v);
     for (int j = 0; j < p.slots; ++j)
       if (s_pos[j] >= 0) reinterpret_cast<uint4*>(p.x16 + (int64_t)s_pos[j] * p.K)[i] = h;
   });
@@ -1128,13 +1281,13 @@ __global__ void __launch_bounds__(kG4PlanThreads) w4_prepare_pairs_kernel(const 
   const G4Row<false, 4> x(p.x + row * p.K, p.K);
   if (pos < 0) return;
   const int e = x.exponent(nullptr);
-  const float f0 = exp2i(e / 2), f1 = exp2i(e - e / 2);
+  const G4Scaler scaled(e);
   if ((threadIdx.x & 31) == 0) {
     p.ex[pos] = e;
     p.order[pos] = (int)row;
   }
   uint4* dst = reinterpret_cast<uint4*>(p.x16 + (int64_t)pos * p.K);
-  x.each([&](const uint4& v, int i) { dst[i] = prepare8(v, f0, f1); });
+  x.each([&](const uint4& v, int i) { dst[i] = scaled(v); });
 }
 
 // y[t] = sum_j weights[t, j] yp[t, j] in the order of j, all in f32: the terms of a token may
@@ -1339,6 +1492,7 @@ cudaError_t launch_g4(const ql_w4_weight& w, const uint16_t* x16, int64_t rows, 
   if (e != cudaSuccess) return e;
   e = make_tmap_u8_sw128(&tx, x16, (uint64_t)w.K * 2, (uint64_t)rows, (uint64_t)w.K * 2, 128, g.ntok);
   if (e != cudaSuccess) return e;
+  p.wq = static_cast<const uint8_t*>(w.wq);
   p.sw = w.sw;
   p.wz = w.wz;
   p.N = w.N;
@@ -1382,15 +1536,25 @@ cudaError_t launch_pdl(void (*kernel)(const G4PrepParams), unsigned grid, unsign
 // 86 against 52.
 constexpr int64_t kW4StreamMaxTokens = 16;
 constexpr int64_t kW4StreamMaxExpertTokens = 16;
+// And the mma.sync kernel, a block of tokens after the other, for rows longer than any
+// layer's: where all of a tile is left out (left_out), its epilogue walks every token's row
+// for every weight row, and that must end well within the 2 s that other warps wait for it.
+constexpr int64_t kW4TensorMaxK = 65536;
 
 size_t w4_workspace_bytes(int64_t M, const ql_w4_weight& w, int sms) {
-  if (M <= kW4StreamMaxTokens) return 0;
+  if (M <= kW4StreamMaxTokens || w.K > kW4TensorMaxK) return 0;
   return g4_layout(M, w.K, 0, 0, 0).total;
 }
 
 cudaError_t launch_w4(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint16_t* y, void* workspace, int sms,
                       DevStatus* status, cudaStream_t st) {
   if (M <= kW4StreamMaxTokens) return launch_w4_stream(x, w, M, y, sms, st);
+  if (w.K > kW4TensorMaxK) {
+    cudaError_t e = cudaSuccess;
+    for (int64_t m = 0; m < M && e == cudaSuccess; m += kW4StreamMaxTokens)
+      e = launch_w4_stream(x + m * w.K, w, std::min(M - m, kW4StreamMaxTokens), y + m * w.N, sms, st);
+    return e;
+  }
   const G4Plan g = plan_dense(M, w, sms);
   const G4Layout L = g4_layout(M, w.K, 0, 0, 0);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1402,6 +1566,7 @@ cudaError_t launch_w4(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint1
   cudaError_t e = launch_pdl(w4_prepare_kernel, (unsigned)M, kG4PrepThreads, q, st);
   if (e != cudaSuccess) return e;
   G4Params p = {};
+  p.x = x;
   p.y = y;
   p.ex = q.ex;
   p.M = M;
@@ -1410,7 +1575,7 @@ cudaError_t launch_w4(const uint16_t* x, const ql_w4_weight& w, int64_t M, uint1
 }
 
 size_t w4_experts_workspace_bytes(int64_t T, int64_t topk, const ql_w4_weight& w, bool combine, int sms) {
-  if (T <= kW4StreamMaxExpertTokens) return 0;
+  if (T <= kW4StreamMaxExpertTokens || w.K > kW4TensorMaxK) return 0;
   const int64_t pairs = T * topk;
   const G4Plan g = plan_experts(pairs, w);
   return g4_layout(pairs, w.K, pairs, g.tok_tiles, combine ? pairs * w.N : 0).total;
@@ -1419,8 +1584,16 @@ size_t w4_experts_workspace_bytes(int64_t T, int64_t topk, const ql_w4_weight& w
 cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float* weights, const ql_w4_weight& w,
                               int64_t T, int64_t topk, uint16_t* y, void* workspace, int sms, DevStatus* status,
                               cudaStream_t st) {
-  if (T <= kW4StreamMaxExpertTokens) return launch_w4_stream_experts(x, ids, weights, w, T, topk, y, sms, st);
   const bool combine = weights != nullptr;
+  if (T <= kW4StreamMaxExpertTokens || w.K > kW4TensorMaxK) {
+    constexpr int64_t kBlock = 1 << 18;  // tokens of a launch: its grid
+    cudaError_t e = cudaSuccess;
+    for (int64_t t = 0; t < T && e == cudaSuccess; t += kBlock)
+      e = launch_w4_stream_experts(x + t * w.K * (combine ? topk : 1), ids + t * topk,
+                                   combine ? weights + t * topk : nullptr, w, std::min(T - t, kBlock), topk,
+                                   y + t * w.N * (combine ? 1 : topk), sms, st);
+    return e;
+  }
   const int64_t pairs = T * topk;
   const G4Plan g = plan_experts(pairs, w);
   const G4Layout L = g4_layout(pairs, w.K, pairs, g.tok_tiles, combine ? pairs * w.N : 0);
@@ -1453,6 +1626,8 @@ cudaError_t launch_w4_experts(const uint16_t* x, const int32_t* ids, const float
   if (e != cudaSuccess) return e;
   G4Params p = {};
   p.y = y;
+  p.x = x;
+  p.slots = q.slots;
   p.yp = combine ? reinterpret_cast<float*>(ws + L.yp) : nullptr;
   p.ex = q.ex;
   p.order = q.order;

@@ -451,8 +451,10 @@ ql_status qlinear_quantize_weight_w4(const uint16_t* w, int64_t N, int64_t K, in
 
 /* Product with 4-bit weights, activations not rounded (weight-only numerics):
  *   y[m,n] = bf16_rne( sum_k x[m,k] * w[n,k] ),
- * products exact, sums in f32.  Any M: a few tokens stream the weights once, more
- * run on the tcgen05 tensor cores.
+ * sums in f32 of exact products, but that with zero points (wz given) and M > 16 (and
+ * K <= 65536) each weight (q - z) s is first rounded to 11 significant bits (it may
+ * have 12).  Any M: up to 16 tokens stream the weights once, more run on the tcgen05
+ * tensor cores (K above 65536: in blocks of 16).
  *   x          device, bf16 [M,K];  y  device, out: bf16 [M,N]
  *   w          experts = 1
  *   workspace  device, qlinear_forward_w4_workspace_bytes(M, w) bytes (0: none
@@ -511,7 +513,9 @@ ql_status qlinear_route(const void* logits, int logits_bf16, const ql_route_conf
  *                  (the gate and up rows, before the activation)
  *   weights given: x [T,top_k,K], y[t,:] = bf16_rne(sum_j weights[t,j] W_e x[t,j])  [T,N]
  *                  (the down rows and the combination, summed in f32)
- * Activations are not rounded and sums are f32, as in qlinear_forward_w4.  An id
+ * Activations are not rounded and sums are f32, as in qlinear_forward_w4; the
+ * rounding of weights with zero points starts at T > 16, and terms of a combined
+ * output are not rounded before their sum.  An id
  * outside [0, experts) takes part in nothing: its rows of y are zero, or its term
  * is left out.  A token may name an expert twice.
  *   ids        device, int32 [T,top_k], as qlinear_route writes them
