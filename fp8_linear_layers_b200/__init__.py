@@ -330,7 +330,10 @@ def forward_workspace_bytes(scheme: int, M: int, N: int, K: int) -> int:
 
 
 def new_workspace(nbytes: int, device="cuda") -> torch.Tensor:
-    """A zero-filled workspace buffer (the library keeps it zero-filled after each call)."""
+    """A zero-filled workspace buffer.  What a call needs zero of it, it leaves zero for the
+    next call of the same entry point and shape.  A buffer that other calls use in between
+    must be zeroed again (`gemm`, `gemm_grouped`, `gemm_quant_out` and the 4-bit calls may
+    share one without)."""
     return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 

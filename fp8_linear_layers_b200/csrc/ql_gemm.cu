@@ -801,6 +801,8 @@ static GemmPlan plan_gemm(ql_scheme s, int64_t M, const int64_t* Ns, int count, 
   const int64_t mt = (M + kGemmBM - 1) / kGemmBM;
   const int64_t tiles = group_tiles(mt, Ns, count, 256);
   const int64_t nkb = (K + kGemmBK - 1) / kGemmBK;
+  static_assert(kWorkspaceTail / 4 >= 256 / 2, "a counter for each split tile of up to 256 SMs");
+  sms = std::min(sms, 256);
   if (2 * tiles <= sms && nkb >= 64) return GemmPlan{256, 2};
   if (s != QL_FP8_E4M3_BLOCK128) return pl;
   // Tiles of the chosen width that fill at most a quarter of the SMs (small
@@ -826,7 +828,7 @@ size_t gemm_group_workspace_bytes(ql_scheme s, int64_t M, const int64_t* Ns, int
   const GemmPlan pl = plan_gemm(s, M, Ns, count, K, sms);
   if (pl.split == 1) return 0;
   const int64_t tiles = group_tiles((M + kGemmBM - 1) / kGemmBM, Ns, count, pl.bn);
-  return align256(split_parts_bytes(tiles, pl.split)) + align256((size_t)tiles * 4);
+  return align256(split_parts_bytes(tiles, pl.split)) + kWorkspaceTail;
 }
 
 size_t gemm_workspace_bytes(ql_scheme s, int64_t M, int64_t N, int64_t K, int sms) {
@@ -908,9 +910,9 @@ cudaError_t launch_gemm_group(ql_scheme scheme, const void* qx, const float* sx,
   p.ntiles = t;
   p.split = pl.split;
   p.parts = pl.split > 1 ? static_cast<float*>(workspace) : nullptr;
-  p.counters = pl.split > 1 ? reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) +
-                                                          align256(split_parts_bytes((int64_t)p.ntiles, pl.split)))
-                            : nullptr;
+  p.counters = pl.split > 1
+                   ? reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + ws_bytes / 256 * 256 - kWorkspaceTail)
+                   : nullptr;
   p.acc_i32 = dbg ? dbg->acc_i32 : nullptr;
   p.acc_f32 = dbg ? dbg->acc_f32 : nullptr;
   p.status = status;

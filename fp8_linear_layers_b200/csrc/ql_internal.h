@@ -80,6 +80,12 @@ cudaError_t launch_gemv_weight_only(ql_scheme scheme, const uint16_t* x, const v
                                     const float* sw, int64_t M, int64_t N, int64_t K, uint16_t* y,
                                     int num_sms, DevStatus* status, cudaStream_t st);
 
+// The last bytes of a large-M workspace (its size rounded down to 256): the arrival counters
+// of the K split's tiles, at most half the SMs, zero between calls.  At the end of the buffer
+// that the caller passes, whatever the shape needs of it, so that no other shape's sums, and
+// no 4-bit call, writes there.
+constexpr size_t kWorkspaceTail = 512;
+
 // Large-M tcgen05 GEMM on pre-quantized activations.
 size_t gemm_workspace_bytes(ql_scheme scheme, int64_t M, int64_t N, int64_t K, int num_sms);
 // a group of 1..QL_GEMM_MAX_GROUP products on one q_x (their N in Ns)

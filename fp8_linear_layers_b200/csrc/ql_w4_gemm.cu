@@ -1441,7 +1441,7 @@ G4Layout g4_layout(int64_t rows, int64_t K, int64_t pairs, unsigned tiles, int64
   off += 256;
   L.yp = off;
   off += up256((size_t)yp_elems * 4);
-  L.total = off;
+  L.total = off + kWorkspaceTail;  // not ours to write
   return L;
 }
 

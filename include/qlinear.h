@@ -250,7 +250,8 @@ size_t qlinear_weight_only_workspace_bytes(ql_scheme scheme, int64_t M, int64_t 
  *              counters) must be zero when a call starts; a call that
  *              completes leaves it ready for the next call of the same shape,
  *              so one workspace serves call after call of one shape.  Zero it
- *              again before a call of another (M, N, K) or after a
+ *              again before a call of another (M, N, K), after another entry
+ *              point has used it (the 4-bit calls fill it), or after a
  *              QL_ERR_TIMEOUT.  Two calls in flight at the same time
  *              must not share a workspace.
  *   dbg        optional (NULL): q_x, s_x, acc_i32 (int8) / acc_f32 (E4M3 row) */
@@ -292,11 +293,16 @@ ql_status qlinear_gemm_small_prequant(ql_scheme scheme, const void* qx, const fl
  *              CTAs that park their partial sums in it (the block scheme's
  *              f32 running sums; the row schemes' raw s32 / f32
  *              accumulators, added before the scales: int8 outputs stay
- *              bit-exact) -- one 128x256 slab per part per output tile, then
- *              one arrival counter per tile; the last to arrive adds the
+ *              bit-exact) -- one 128x256 slab per part per output tile, and
+ *              an arrival counter per tile in the last 512 bytes (of ws_bytes
+ *              rounded down to 256); the last to arrive adds the
  *              parts in part order (the same bits whatever the order of
  *              arrival).  A completed call leaves the counters zero again,
- *              for any next shape; zero the workspace again after a
+ *              for any next shape of qlinear_gemm, qlinear_gemm_grouped or
+ *              qlinear_gemm_quant_out that is given the same ws_bytes, and the
+ *              4-bit calls (qlinear_forward_w4, qlinear_experts_w4) leave them
+ *              alone.  Zero the workspace again after any other call that used
+ *              it, and after a
  *              QL_ERR_TIMEOUT.  Two calls in flight at the same time must not
  *              share it.  qlinear_workspace_bytes returns 0 for shapes that
  *              run whole tiles.
@@ -459,8 +465,10 @@ ql_status qlinear_quantize_weight_w4(const uint16_t* w, int64_t N, int64_t K, in
  *   w          experts = 1
  *   workspace  device, qlinear_forward_w4_workspace_bytes(M, w) bytes (0: none
  *              needed, NULL allowed), 256-byte aligned.  Scratch: its contents
- *              before a call do not matter.  Calls in flight together must not
- *              share it.
+ *              before a call do not matter, and a call leaves its own there, but
+ *              for the last 512 bytes.  A workspace that an 8-bit call needs
+ *              zero-filled must be zeroed again behind this one (qlinear_gemm's
+ *              needs nothing).  Calls in flight together must not share it.
  * Unlike the 8-bit products, wq, sw and wz may be written by earlier work on the
  * same stream.
  * Errors: argument checks as above; M = 0 is a no-op; QL_ERR_WORKSPACE. */
