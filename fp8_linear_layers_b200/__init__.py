@@ -17,6 +17,7 @@ scales as ``torch.float32``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -529,6 +530,9 @@ def forward(scheme: int, x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
 
 
 # ---------------------------------------------------------------- 4-bit weights, experts
+#
+# `stream`: a torch stream, a stream's handle, or None for the current one.  Inputs must be
+# ready there; outputs that a call makes belong to it, as if made under torch.cuda.stream.
 
 
 def _on(t: torch.Tensor, dtype, name: str, device: int) -> int:
@@ -539,10 +543,25 @@ def _on(t: torch.Tensor, dtype, name: str, device: int) -> int:
     return p
 
 
-def _out(t, shape: tuple, dtype, like: torch.Tensor, name: str, device: int):
+def _allocating_on(stream):
+    """The context in which a call's scratch and outputs are made: those of a call on another
+    stream come from that stream's memory, which the caching allocator hands out again only
+    behind the call's work.  (A block of the current stream's could still be in use there.)"""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _out(t, shape: tuple, dtype, like: torch.Tensor, name: str, device: int, stream):
     """An output and its address: the caller's, checked, or a new one beside `like`."""
     if t is None:
-        t = like.new_empty(shape, dtype=dtype)
+        if stream is None:
+            t = like.new_empty(shape, dtype=dtype)
+        else:
+            with _allocating_on(stream):
+                t = like.new_empty(shape, dtype=dtype)
         return t, t.data_ptr()
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {shape}")
@@ -605,9 +624,10 @@ def quantize_weight_w4(w: torch.Tensor, group: int = 128, zeros: bool = False, s
     lead = tuple(w.shape[:-1])
     dev = torch._C._cuda_getDevice()
     wp = _on(w, torch.bfloat16, "w", dev)
-    wq = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=w.device)
-    sw = torch.empty(lead + (-(-K // group),), dtype=torch.bfloat16, device=w.device)
-    wz = torch.empty_like(sw, dtype=torch.uint8) if zeros else None
+    with _allocating_on(stream):
+        wq = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=w.device)
+        sw = torch.empty(lead + (-(-K // group),), dtype=torch.bfloat16, device=w.device)
+        wz = torch.empty_like(sw, dtype=torch.uint8) if zeros else None
     _check(lib().qlinear_quantize_weight_w4(wp, w.numel() // K, K, group, wq.data_ptr(), sw.data_ptr(),
                                             None if wz is None else wz.data_ptr(), _launch_stream(stream, dev)),
            "qlinear_quantize_weight_w4")
@@ -632,20 +652,15 @@ def forward_w4(x: torch.Tensor, w: W4Weight, workspace: torch.Tensor | None = No
         nb = L.qlinear_forward_w4_workspace_bytes(M, w._p)
         workspace = _scratch(nb, stream) if nb else None
     xp = _on(x, torch.bfloat16, "x", dev)
-    y, yp = _out(y, (M, w.N), torch.bfloat16, x, "y", dev)
+    y, yp = _out(y, (M, w.N), torch.bfloat16, x, "y", dev, stream)
     wp, wn = (None, 0) if workspace is None else (_on(workspace, torch.uint8, "workspace", dev), workspace.numel())
     _check(L.qlinear_forward_w4(xp, w._p, M, yp, wp, wn, _launch_stream(stream, dev)), "qlinear_forward_w4")
     return y
 
 
 def _scratch(nbytes: int, stream) -> torch.Tensor:
-    """Scratch for one call, allocated on the call's stream so that the caching
-    allocator hands it out again only behind the call's work."""
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(stream):
+    """Scratch for one call."""
+    with _allocating_on(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
 
@@ -683,8 +698,8 @@ def route(logits: torch.Tensor, top_k: int, score: int = ROUTE_SOFTMAX, bias: to
         bp = _on(bias, torch.float32, "bias", dev)
         if bias.numel() != E:
             raise ValueError(f"bias must have {E} entries")
-    ids, ip = _out(ids, (T, top_k), torch.int32, logits, "ids", dev)
-    weights, wp = _out(weights, (T, top_k), torch.float32, logits, "weights", dev)
+    ids, ip = _out(ids, (T, top_k), torch.int32, logits, "ids", dev, stream)
+    weights, wp = _out(weights, (T, top_k), torch.float32, logits, "weights", dev, stream)
     c = _route_config(E, top_k, groups, top_groups, group_top, score, renormalize, scale)
     _check(lib().qlinear_route(lp, bf16, c.address, bp, T, ip, wp, _launch_stream(stream, dev)), "qlinear_route")
     return ids, weights
@@ -717,7 +732,7 @@ def experts_w4(x: torch.Tensor, ids: torch.Tensor, w: W4Weight, weights: torch.T
         workspace = _scratch(nb, stream) if nb else None
     shape = (T, w.N) if combine else (T, k, w.N)
     xp, ip = _on(x, torch.bfloat16, "x", dev), _on(ids, torch.int32, "ids", dev)
-    y, yp = _out(y, shape, torch.bfloat16, x, "y", dev)
+    y, yp = _out(y, shape, torch.bfloat16, x, "y", dev, stream)
     wp, wn = (None, 0) if workspace is None else (_on(workspace, torch.uint8, "workspace", dev), workspace.numel())
     _check(L.qlinear_experts_w4(xp, ip, gp, w._p, T, k, yp, wp, wn, _launch_stream(stream, dev)), "qlinear_experts_w4")
     return y
