@@ -20,6 +20,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import operator
 import os
 from dataclasses import dataclass
 
@@ -675,10 +676,18 @@ class _RouteConfig(ctypes.Structure):
 
 
 @functools.lru_cache(maxsize=256)
-def _route_config(*fields) -> _RouteConfig:
+def _route_config_of(*fields) -> _RouteConfig:
     c = _RouteConfig(*fields)
     c.address = ctypes.addressof(c)
     return c
+
+
+def _route_config(experts, top_k, groups, top_groups, group_top, score, renormalize, scale) -> _RouteConfig:
+    # kept by their values: a tensor or an array would be kept by its identity, and answer with
+    # what it held at the first call
+    index = operator.index
+    return _route_config_of(experts, index(top_k), index(groups), index(top_groups), index(group_top), index(score),
+                            bool(renormalize), float(scale))
 
 
 def route(logits: torch.Tensor, top_k: int, score: int = ROUTE_SOFTMAX, bias: torch.Tensor | None = None,
