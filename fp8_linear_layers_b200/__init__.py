@@ -591,17 +591,18 @@ class W4Weight:
 
     wq uint8 [N,K/2] (low nibble: even k) or, for experts, [E,N,K/2]; sw bfloat16
     [(E,)N,ceil(K/group)]; wz uint8 of sw's shape, or None for a zero point of 8.
-    The tensors are checked once and kept; their contents may change."""
+    The tensors are checked once and kept; their contents may change, but not which tensors
+    they are, nor where their memory is (calls refuse that)."""
 
-    __slots__ = ("wq", "sw", "wz", "group", "experts", "N", "K", "device", "_c", "_p")
+    __slots__ = ("wq", "sw", "wz", "group", "experts", "N", "K", "device", "_c", "_p", "_at")
 
     def __init__(self, wq: torch.Tensor, sw: torch.Tensor, wz: torch.Tensor | None = None, group: int = 128):
         if group not in W4_GROUPS:
             raise ValueError(f"group must be one of {W4_GROUPS}")
-        if wq.dim() not in (2, 3):
-            raise ValueError("wq must be [N,K/2] or [E,N,K/2]")
         if not isinstance(wq, torch.Tensor) or not wq.is_cuda:
             raise TypeError("wq must be a CUDA tensor")
+        if wq.dim() not in (2, 3):
+            raise ValueError("wq must be [N,K/2] or [E,N,K/2]")
         K = 2 * wq.shape[-1]
         shape = tuple(wq.shape[:-1]) + (-(-K // group),)
         if tuple(sw.shape) != shape or (wz is not None and tuple(wz.shape) != shape):
@@ -613,6 +614,21 @@ class W4Weight:
         self._c = _W4(_on(wq, torch.uint8, "wq", self.device), _on(sw, torch.bfloat16, "sw", self.device),
                       None if wz is None else _on(wz, torch.uint8, "wz", self.device), self.experts, self.N, K, group)
         self._p = ctypes.addressof(self._c)
+        self._at = (wq.data_ptr(), sw.data_ptr(), 0 if wz is None else wz.data_ptr())
+
+    def _address(self) -> int:
+        """The C struct, whose pointers are still the tensors'."""
+        q, s, z = self._at
+        if self.wq.data_ptr() != q or self.sw.data_ptr() != s or (z and self.wz.data_ptr() != z):
+            raise ValueError("the weights' tensors have other memory than when they were checked; make a new W4Weight")
+        return self._p
+
+    def __setattr__(self, name, value):
+        if hasattr(self, name):  # the C struct would keep the old tensor's address
+            raise AttributeError(f"{name} cannot be replaced; make a new W4Weight")
+        object.__setattr__(self, name, value)
+
+    __delattr__ = None
 
 
 def quantize_weight_w4(w: torch.Tensor, group: int = 128, zeros: bool = False, stream=None) -> W4Weight:
@@ -655,7 +671,7 @@ def forward_w4(x: torch.Tensor, w: W4Weight, workspace: torch.Tensor | None = No
     xp = _on(x, torch.bfloat16, "x", dev)
     y, yp = _out(y, (M, w.N), torch.bfloat16, x, "y", dev, stream)
     wp, wn = (None, 0) if workspace is None else (_on(workspace, torch.uint8, "workspace", dev), workspace.numel())
-    _check(L.qlinear_forward_w4(xp, w._p, M, yp, wp, wn, _launch_stream(stream, dev)), "qlinear_forward_w4")
+    _check(L.qlinear_forward_w4(xp, w._address(), M, yp, wp, wn, _launch_stream(stream, dev)), "qlinear_forward_w4")
     return y
 
 
@@ -743,7 +759,7 @@ def experts_w4(x: torch.Tensor, ids: torch.Tensor, w: W4Weight, weights: torch.T
     xp, ip = _on(x, torch.bfloat16, "x", dev), _on(ids, torch.int32, "ids", dev)
     y, yp = _out(y, shape, torch.bfloat16, x, "y", dev, stream)
     wp, wn = (None, 0) if workspace is None else (_on(workspace, torch.uint8, "workspace", dev), workspace.numel())
-    _check(L.qlinear_experts_w4(xp, ip, gp, w._p, T, k, yp, wp, wn, _launch_stream(stream, dev)), "qlinear_experts_w4")
+    _check(L.qlinear_experts_w4(xp, ip, gp, w._address(), T, k, yp, wp, wn, _launch_stream(stream, dev)), "qlinear_experts_w4")
     return y
 
 
