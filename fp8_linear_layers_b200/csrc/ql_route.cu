@@ -167,7 +167,7 @@ __device__ __noinline__ void select_f64(const RouteParams& p, const void* row, f
             b = v;
           }
         }
-        gs = p.group_top == 1 ? a : a + b;
+        gs = p.group_top == 1 ? a : b == kNone ? kNone : a + b;  // (a may be +inf)
       }
       uint32_t mask = 0;
       bool taken = lane >= p.G;
@@ -331,11 +331,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
       __syncwarp();
     }
     if (member) {
-      const float gs = p.group_top == 1 ? a : a + b;
+      // the mean of two stands for their sum: it is in range wherever they are (a mask may be
+      // the lowest f32); short of two, -inf, though the one be +inf
+      const float gs = p.group_top == 1 ? a : usable(b) ? 0.5f * a + 0.5f * b : none;
       gkey = order_key(gs);
-      // scores are at most 1; without a bias a single largest is a logit, and exact
-      if (scores && usable(gs))
-        gerr = p.group_top == 1 ? err + kRoundErr * fabsf(a) : 2.0f * err + kRoundErr * (fabsf(a) + fabsf(b));
+      // scores are at most 1; without a bias a single largest is a logit, and exact; so are
+      // infinities
+      if (scores && fabsf(gs) < -none)
+        gerr = err + kRoundErr * (p.group_top == 1 ? fabsf(a) : 0.5f * fabsf(a) + 0.5f * fabsf(b));
     }
     uint32_t kept = 0;  // by group
     float low = 0.0f;   // the smallest value kept, less its error
