@@ -535,16 +535,6 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             o[i] = scale2(__uint_as_float(v[i]), -(f + (c + i < count ? s_ex[c + i] >> 1 : 0)));
-#pragma unroll 1
-          for (int i = 0; i < min(16, count - c); ++i) {
-            const int ex = s_ex[c + i];
-            if (!(ex & 1) && !rows_out) continue;
-            const float more = left_out<kGroup, kZero>(p.x + (m0 + c + i) * p.K, p.wq + wr * (p.K >> 1), sw, wz, ex, fl,
-                                                       kr.w0 * kG4StageK, min((int)p.K, (kr.w0 + kr.n) * kG4StageK));
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (j == i) o[j] += more;
-          }
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -553,6 +543,22 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
             part[(c + i) * 128 + col] = o[i];
           else
             *reinterpret_cast<uint16_t*>(wring + (c + i) * kRow + col * 2) = f32_to_bf16_rn(o[i]);
+        }
+      }
+      if (wide) {  // tokens with something left out once more
+        __syncwarp();
+#pragma unroll 1
+        for (int c = c_lo; c < min(c_hi, count); ++c) {
+          const int ex = s_ex[c];
+          if (!(ex & 1) && !rows_out) continue;
+          const float o = scale2(w4::ld1(tmem + lane_addr + c), -(f + (ex >> 1))) +
+                          left_out<kGroup, kZero>(p.x + (m0 + c) * p.K, p.wq + wr * (p.K >> 1), sw, wz, ex, fl,
+                                                  kr.w0 * kG4StageK, min((int)p.K, (kr.w0 + kr.n) * kG4StageK));
+          if (p.splits > 1)
+            part[c * 128 + col] = o;
+          else
+            *reinterpret_cast<uint16_t*>(wring + c * kRow + col * 2) = f32_to_bf16_rn(o);
+          __syncwarp();  // ld1 is a whole-warp instruction
         }
       }
       tc::fence_before();
@@ -916,7 +922,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         uint32_t v[16];
         w4::ld16(tmem + r * kWideTok + lane_addr + c, v);
         tc::ld_wait();
-        if (c + 16 >= mma_n) {
+        if (c + 16 >= mma_n && !wide) {
           tc::fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&dempty[r]);
@@ -935,18 +941,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             o[i] = scale2(__uint_as_float(v[i]), -(f + (c + i < w.count ? s_ex[buf + c + i] >> 1 : 0)));
-#pragma unroll 1
-          for (int i = 0; i < min(16, w.count - c); ++i) {
-            const int ex = s_ex[buf + c + i];
-            if (!(ex & 1) && !rows_out) continue;
-            const int64_t wr = w.e * p.N + min(nw + lane, p.N - 1);
-            const int64_t xr = kExperts ? s_out[buf + c + i] / p.slots : w.m0 + c + i;
-            const float more = left_out<kGroup, kZero>(p.x + xr * p.K, p.wq + wr * (p.K >> 1), p.sw + wr * p.groups,
-                                                       kZero ? p.wz + wr * p.groups : nullptr, ex, fl, 0, (int)p.K);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (j == i) o[j] += more;
-          }
         }
         if (kExperts && p.yp) {  // f32: half the tokens at a time fit the staging
 #pragma unroll
@@ -992,6 +986,29 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             p.y[orow * p.N + nw + lane] = f32_to_bf16_rn(o[i]);
           }
         }
+      }
+      if (wide) {  // tokens with something left out once more, then the accumulators are free
+        __syncwarp();  // (other lanes wrote these outputs above)
+#pragma unroll 1
+        for (int c = 0; c < w.count; ++c) {
+          const int ex = s_ex[buf + c];
+          if (!(ex & 1) && !rows_out) continue;
+          const int64_t wr = w.e * p.N + min(nw + lane, p.N - 1), orow = kExperts ? s_out[buf + c] : w.m0 + c;
+          const float o = scale2(w4::ld1(tmem + r * kWideTok + lane_addr + c), -(f + (ex >> 1))) +
+                          left_out<kGroup, kZero>(p.x + (kExperts ? orow / p.slots : orow) * p.K, p.wq + wr * (p.K >> 1),
+                                                  p.sw + wr * p.groups, kZero ? p.wz + wr * p.groups : nullptr, ex, fl,
+                                                  0, (int)p.K);
+          if (nw + lane < p.N) {
+            if (kExperts && p.yp)
+              p.yp[orow * p.N + nw + lane] = o;
+            else
+              p.y[orow * p.N + nw + lane] = f32_to_bf16_rn(o);
+          }
+          __syncwarp();  // ld1 is a whole-warp instruction
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&dempty[r]);
       }
     }
     if (!ok) {
