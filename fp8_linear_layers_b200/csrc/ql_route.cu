@@ -21,7 +21,8 @@
 // last chosen and the best left out, are closer than that, the candidates that can
 // matter (at most 32, one to a lane) get their f64 values and are ranked by those; where
 // groups are that close, or more than 32 candidates, the token is selected again from
-// f64 values throughout.
+// f64 values throughout (4099 x 256, sigmoid, bias, groups: 13.4 us, 18 to 20 with such a
+// token).  Up to 128 experts, and from 257 to 512, 8 to 16 bytes a thread spill.
 #include "ql_internal.h"
 #include "ql_w4.cuh"
 

@@ -6,7 +6,8 @@
 //
 // with IEEE f32 divisions; a group whose scale is zero gets codes (and zero
 // points) 8.  One thread takes 8 inputs (16 bytes), group / 8 neighbouring lanes
-// take a group.  Bound by the 2 N K bytes it reads.
+// take a group.  Offline: 14336 x 4096 101 us, with zero points 106 (1.4 TB/s read and
+// written); a division to a weight, not the bytes, takes the time.
 #include "ql_internal.h"
 #include "ql_w4.cuh"
 

@@ -21,13 +21,15 @@
 // meet in shared memory and are added in warp order, so a result does not depend on
 // timing.
 //
-// What bounds it: instructions, not the memory (the weights in L2 or in HBM: the same
-// time).  A word of eight codes takes 11 of them to become bf16 and 1 to be multiplied;
-// with the loads, addresses and scales about 16, at one or two a cycle and SM while a
-// launch starts, fills and drains in a third of the time.  Hence one address a row and
-// chunk, bounds only at a row's end, and scales of neighbouring groups in one load (one
-// token, group 128: 4096 x 14336 14.7 -> 12.2 us, a combined product of 7 tokens with 8
-// experts 2048 x 768 18.5 -> 14.1 us).
+// What bounds it: no one unit (SM throughput 27 to 33 %, DRAM 17 to 22 %, a fifth of the
+// warps, first stall the long scoreboard; the weights in L2 or in HBM: the same time).  A
+// launch's start, fill and drain are a third of the time; CTAs do not divide by the SMs (4096
+// rows: 256 CTAs, so 40 of 148 SMs hold one and 108 two); and a word of eight codes takes 11
+// instructions to become bf16 and 1 to be multiplied, with the loads, addresses and scales
+// about 16.  Fewer of those did help: one address a row and chunk, bounds only at a row's
+// end, and scales of neighbouring groups in one load (one token, group 128: 4096 x 14336
+// 14.7 -> 12.2 us, a combined product of 7 tokens with 8 experts 2048 x 768 18.5 -> 14.1 us).
+// The variants of 32 rows and zero points and of 16 tokens spill 8 to 104 bytes a thread.
 // 14336 x 4096, group 128: 1 token 11.2 us (2.7 TB/s), 8 tokens 12.3 us, 16 tokens 17.4 us;
 // 1024 x 4096 1 token 2.6 us.
 #include "ql_internal.h"
