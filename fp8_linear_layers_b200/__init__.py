@@ -14,6 +14,10 @@ Schemes (see the header for the exact numerics):
 Tensors: bf16 activations/outputs as ``torch.bfloat16``; quantized codes as
 ``torch.uint8`` (view them as ``torch.int8`` / ``torch.float8_e4m3fn``);
 scales as ``torch.float32``.
+
+Streams: ``stream`` is a torch stream, a stream's handle, or None for the current
+one.  Inputs must be ready on it; outputs that a call makes belong to it, as if
+made under ``torch.cuda.stream``.
 """
 from __future__ import annotations
 
@@ -156,6 +160,25 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _allocating_on(stream):
+    """The context in which a call's scratch and outputs are made: those of a call on another
+    stream come from that stream's memory, which the caching allocator hands out again only
+    behind the call's work.  (A block of the current stream's could still be in use there.)"""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _new(stream, shape: tuple, dtype, device) -> torch.Tensor:
+    """A new output of a call on `stream`."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _allocating_on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dev(t: torch.Tensor, dtype, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -177,8 +200,8 @@ def act_scale_shape(scheme: int, M: int, K: int) -> tuple:
 def quantize_weight(scheme: int, w: torch.Tensor, stream=None):
     """W bf16 [N,K] -> (W_q uint8 [N,K], s_w f32 [N] or [N/128,K/128])."""
     N, K = w.shape
-    wq = torch.empty((N, K), dtype=torch.uint8, device=w.device)
-    sw = torch.empty(weight_scale_shape(scheme, N, K), dtype=torch.float32, device=w.device)
+    wq = _new(stream, (N, K), dtype=torch.uint8, device=w.device)
+    sw = _new(stream, weight_scale_shape(scheme, N, K), dtype=torch.float32, device=w.device)
     _check(lib().qlinear_quantize_weight(scheme, _dev(w, torch.bfloat16, "w"), N, K, wq.data_ptr(),
                                          sw.data_ptr(), _stream(stream)), "qlinear_quantize_weight")
     return wq, sw
@@ -188,9 +211,9 @@ def quantize_act(scheme: int, x: torch.Tensor, qx=None, sx=None, stream=None):
     """X bf16 [M,K] -> (q_x uint8 [M,K], s_x f32 [M] or [M,K/128])."""
     M, K = x.shape
     if qx is None:
-        qx = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        qx = _new(stream, (M, K), dtype=torch.uint8, device=x.device)
     if sx is None:
-        sx = torch.empty(act_scale_shape(scheme, M, K), dtype=torch.float32, device=x.device)
+        sx = _new(stream, act_scale_shape(scheme, M, K), dtype=torch.float32, device=x.device)
     _check(lib().qlinear_quantize_act(scheme, _dev(x, torch.bfloat16, "x"), M, K,
                                       _dev(qx, torch.uint8, "qx"), _dev(sx, torch.float32, "sx"),
                                       _stream(stream)), "qlinear_quantize_act")
@@ -205,7 +228,7 @@ def gemv(scheme: int, x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor, y=Non
     if x.numel() != K:
         raise ValueError("gemv takes a single token")
     if y is None:
-        y = torch.empty((1, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(stream, (1, N), dtype=torch.bfloat16, device=x.device)
     _check(lib().qlinear_gemv(scheme, _dev(x, torch.bfloat16, "x"), _dev(wq, torch.uint8, "wq"),
                               _dev(sw, torch.float32, "sw"), N, K, _dev(y, torch.bfloat16, "y"),
                               debug._c() if debug else None, _stream(stream)), "qlinear_gemv")
@@ -237,7 +260,7 @@ def gemv_grouped(scheme: int, problems, stream=None) -> list:
             raise ValueError("every product of a grouped launch takes one token of the same K")
         N = wq.shape[0]
         if y is None:
-            y = torch.empty((1, N), dtype=torch.bfloat16, device=xin.device)
+            y = _new(stream, (1, N), dtype=torch.bfloat16, device=xin.device)
         if qx is None:
             table[j] = _GemvProblem(_dev(x, torch.bfloat16, "x"), None, None, _dev(wq, torch.uint8, "wq"),
                                     _dev(sw, torch.float32, "sw"), _dev(y, torch.bfloat16, "y"), N)
@@ -259,7 +282,7 @@ def gemv_prequant(scheme: int, qx: torch.Tensor, sx: torch.Tensor, wq: torch.Ten
     if qx.numel() != K:
         raise ValueError("gemv_prequant takes a single token")
     if y is None:
-        y = torch.empty((1, N), dtype=torch.bfloat16, device=qx.device)
+        y = _new(stream, (1, N), dtype=torch.bfloat16, device=qx.device)
     _check(lib().qlinear_gemv_prequant(scheme, _dev(qx, torch.uint8, "qx"), _dev(sx, torch.float32, "sx"),
                                        _dev(wq, torch.uint8, "wq"), _dev(sw, torch.float32, "sw"), N, K,
                                        _dev(y, torch.bfloat16, "y"), _stream(stream)),
@@ -276,7 +299,7 @@ def gemv_weight_only(scheme: int, x: torch.Tensor, wq: torch.Tensor, sw: torch.T
     if x.numel() != K:
         raise ValueError("gemv_weight_only takes a single token")
     if y is None:
-        y = torch.empty((1, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(stream, (1, N), dtype=torch.bfloat16, device=x.device)
     _check(lib().qlinear_gemv_weight_only(scheme, _dev(x, torch.bfloat16, "x"),
                                           _dev(wq, torch.uint8, "wq"), _dev(sw, torch.float32, "sw"),
                                           N, K, _dev(y, torch.bfloat16, "y"), _stream(stream)),
@@ -291,7 +314,7 @@ def debug_gemv_stalled(scheme: int, x: torch.Tensor, wq: torch.Tensor, sw: torch
     K = x.shape[-1]
     N = wq.shape[0]
     if y is None:
-        y = torch.empty((1, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(stream, (1, N), dtype=torch.bfloat16, device=x.device)
     _check(lib().qlinear_debug_gemv_stalled(scheme, _dev(x, torch.bfloat16, "x"),
                                             _dev(wq, torch.uint8, "wq"), _dev(sw, torch.float32, "sw"),
                                             N, K, _dev(y, torch.bfloat16, "y"), _stream(stream)),
@@ -306,10 +329,11 @@ def forward_weight_only(scheme: int, x: torch.Tensor, wq: torch.Tensor, sw: torc
     M, K = x.shape
     N = wq.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(stream, (M, N), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         nb = weight_only_workspace_bytes(scheme, M, N, K)
-        workspace = new_workspace(nb) if nb else None
+        with _allocating_on(stream):
+            workspace = new_workspace(nb) if nb else None
     wp, wn = _ws(workspace)
     _check(lib().qlinear_forward_weight_only(scheme, _dev(x, torch.bfloat16, "x"),
                                              _dev(wq, torch.uint8, "wq"),
@@ -351,7 +375,7 @@ def gemm_small(scheme: int, x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
     M, K = x.shape
     N = wq.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(stream, (M, N), dtype=torch.bfloat16, device=x.device)
     wp, wn = _ws(workspace)
     _check(lib().qlinear_gemm_small(scheme, _dev(x, torch.bfloat16, "x"), _dev(wq, torch.uint8, "wq"),
                                     _dev(sw, torch.float32, "sw"), M, N, K,
@@ -367,7 +391,7 @@ def gemm_small_prequant(scheme: int, qx: torch.Tensor, sx: torch.Tensor, wq: tor
     M, K = qx.shape
     N = wq.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=qx.device)
+        y = _new(stream, (M, N), dtype=torch.bfloat16, device=qx.device)
     wp, wn = _ws(workspace)
     _check(lib().qlinear_gemm_small_prequant(scheme, _dev(qx, torch.uint8, "qx"), _dev(sx, torch.float32, "sx"),
                                              _dev(wq, torch.uint8, "wq"), _dev(sw, torch.float32, "sw"),
@@ -383,7 +407,7 @@ def gemm_small_noalloc(scheme: int, x: torch.Tensor, wq: torch.Tensor, sw: torch
     M, K = x.shape
     N = wq.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(stream, (M, N), dtype=torch.bfloat16, device=x.device)
     status = lib().qlinear_gemm_small_noalloc(scheme, _dev(x, torch.bfloat16, "x"),
                                               _dev(wq, torch.uint8, "wq"), _dev(sw, torch.float32, "sw"),
                                               M, N, K, _dev(y, torch.bfloat16, "y"), _stream(stream))
@@ -400,7 +424,7 @@ def gemm(scheme: int, qx: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: 
     M, K = qx.shape
     N = wq.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=qx.device)
+        y = _new(stream, (M, N), dtype=torch.bfloat16, device=qx.device)
     wp, wn = _ws(workspace)
     _check(lib().qlinear_gemm(scheme, _dev(qx, torch.uint8, "qx"), _dev(sx, torch.float32, "sx"),
                               _dev(wq, torch.uint8, "wq"), _dev(sw, torch.float32, "sw"), M, N, K,
@@ -442,7 +466,7 @@ def gemm_grouped(scheme: int, qx: torch.Tensor, sx: torch.Tensor, problems, work
             raise ValueError("every product of a grouped launch reads the same [M,K] input")
         N = wq.shape[0]
         if y is None:
-            y = torch.empty((M, N), dtype=torch.bfloat16, device=qx.device)
+            y = _new(stream, (M, N), dtype=torch.bfloat16, device=qx.device)
         elif y is False:
             y = None
         table[j] = _GemmProblem(_dev(wq, torch.uint8, "wq"), _dev(sw, torch.float32, "sw"),
@@ -479,7 +503,7 @@ def gemm_small_grouped(scheme: int, x, problems, workspace: torch.Tensor, stream
             raise ValueError("every product of a grouped launch reads the same [M,K] tokens")
         N = wq.shape[0]
         if y is None:
-            y = torch.empty((M, N), dtype=torch.bfloat16, device=xin.device)
+            y = _new(stream, (M, N), dtype=torch.bfloat16, device=xin.device)
         table[j] = _GemmProblem(_dev(wq, torch.uint8, "wq"), _dev(sw, torch.float32, "sw"),
                                 _dev(y, torch.bfloat16, "y"), None, None, N)
         ys.append(y)
@@ -501,11 +525,11 @@ def gemm_quant_out(scheme: int, qx: torch.Tensor, sx: torch.Tensor, wq: torch.Te
     M, K = qx.shape
     N = wq.shape[0]
     if want_y and y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=qx.device)
+        y = _new(stream, (M, N), dtype=torch.bfloat16, device=qx.device)
     if qy is None:
-        qy = torch.empty((M, N), dtype=torch.uint8, device=qx.device)
+        qy = _new(stream, (M, N), dtype=torch.uint8, device=qx.device)
     if sy is None:
-        sy = torch.empty((M, N // 128), dtype=torch.float32, device=qx.device)
+        sy = _new(stream, (M, N // 128), dtype=torch.float32, device=qx.device)
     wp, wn = _ws(workspace)
     _check(lib().qlinear_gemm_quant_out(scheme, _dev(qx, torch.uint8, "qx"), _dev(sx, torch.float32, "sx"),
                                         _dev(wq, torch.uint8, "wq"), _dev(sw, torch.float32, "sw"), M, N, K,
@@ -521,7 +545,7 @@ def forward(scheme: int, x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
     M, K = x.shape
     N = wq.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(stream, (M, N), dtype=torch.bfloat16, device=x.device)
     wp, wn = _ws(workspace)
     _check(lib().qlinear_forward(scheme, _dev(x, torch.bfloat16, "x"), _dev(wq, torch.uint8, "wq"),
                                  _dev(sw, torch.float32, "sw"), M, N, K,
@@ -531,9 +555,6 @@ def forward(scheme: int, x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
 
 
 # ---------------------------------------------------------------- 4-bit weights, experts
-#
-# `stream`: a torch stream, a stream's handle, or None for the current one.  Inputs must be
-# ready there; outputs that a call makes belong to it, as if made under torch.cuda.stream.
 
 
 def _on(t: torch.Tensor, dtype, name: str, device: int) -> int:
@@ -544,25 +565,10 @@ def _on(t: torch.Tensor, dtype, name: str, device: int) -> int:
     return p
 
 
-def _allocating_on(stream):
-    """The context in which a call's scratch and outputs are made: those of a call on another
-    stream come from that stream's memory, which the caching allocator hands out again only
-    behind the call's work.  (A block of the current stream's could still be in use there.)"""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream)
-
-
 def _out(t, shape: tuple, dtype, like: torch.Tensor, name: str, device: int, stream):
     """An output and its address: the caller's, checked, or a new one beside `like`."""
     if t is None:
-        if stream is None:
-            t = like.new_empty(shape, dtype=dtype)
-        else:
-            with _allocating_on(stream):
-                t = like.new_empty(shape, dtype=dtype)
+        t = like.new_empty(shape, dtype=dtype) if stream is None else _new(stream, shape, dtype, like.device)
         return t, t.data_ptr()
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {shape}")
@@ -641,10 +647,9 @@ def quantize_weight_w4(w: torch.Tensor, group: int = 128, zeros: bool = False, s
     lead = tuple(w.shape[:-1])
     dev = torch._C._cuda_getDevice()
     wp = _on(w, torch.bfloat16, "w", dev)
-    with _allocating_on(stream):
-        wq = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=w.device)
-        sw = torch.empty(lead + (-(-K // group),), dtype=torch.bfloat16, device=w.device)
-        wz = torch.empty_like(sw, dtype=torch.uint8) if zeros else None
+    wq = _new(stream, lead + (K // 2,), torch.uint8, w.device)
+    sw = _new(stream, lead + (-(-K // group),), torch.bfloat16, w.device)
+    wz = _new(stream, tuple(sw.shape), torch.uint8, w.device) if zeros else None
     _check(lib().qlinear_quantize_weight_w4(wp, w.numel() // K, K, group, wq.data_ptr(), sw.data_ptr(),
                                             None if wz is None else wz.data_ptr(), _launch_stream(stream, dev)),
            "qlinear_quantize_weight_w4")
@@ -667,18 +672,12 @@ def forward_w4(x: torch.Tensor, w: W4Weight, workspace: torch.Tensor | None = No
     L = lib()
     if workspace is None:
         nb = L.qlinear_forward_w4_workspace_bytes(M, w._p)
-        workspace = _scratch(nb, stream) if nb else None
+        workspace = _new(stream, (nb,), torch.uint8, x.device) if nb else None
     xp = _on(x, torch.bfloat16, "x", dev)
     y, yp = _out(y, (M, w.N), torch.bfloat16, x, "y", dev, stream)
     wp, wn = (None, 0) if workspace is None else (_on(workspace, torch.uint8, "workspace", dev), workspace.numel())
     _check(L.qlinear_forward_w4(xp, w._address(), M, yp, wp, wn, _launch_stream(stream, dev)), "qlinear_forward_w4")
     return y
-
-
-def _scratch(nbytes: int, stream) -> torch.Tensor:
-    """Scratch for one call."""
-    with _allocating_on(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
 
 ROUTE_SOFTMAX = 0
@@ -754,7 +753,7 @@ def experts_w4(x: torch.Tensor, ids: torch.Tensor, w: W4Weight, weights: torch.T
             raise ValueError(f"weights must be {(T, k)}")
     if workspace is None:
         nb = L.qlinear_experts_w4_workspace_bytes(T, k, w._p, combine)
-        workspace = _scratch(nb, stream) if nb else None
+        workspace = _new(stream, (nb,), torch.uint8, x.device) if nb else None
     shape = (T, w.N) if combine else (T, k, w.N)
     xp, ip = _on(x, torch.bfloat16, "x", dev), _on(ids, torch.int32, "ids", dev)
     y, yp = _out(y, shape, torch.bfloat16, x, "y", dev, stream)
