@@ -1311,7 +1311,7 @@ __global__ void __launch_bounds__(kG4PlanThreads) w4_prepare_pairs_kernel(const 
 // cancel, so a rounded term could be off by more than the whole result's rounding.  A thread
 // takes kVec neighbouring outputs; bound by the pairs' bytes.
 template <int kVec>
-__global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict__ yp, const int32_t* __restrict__ ids,
+__global__ void __launch_bounds__(256, 5) w4_combine_kernel(const float* __restrict__ yp, const int32_t* __restrict__ ids,
                                                          const float* __restrict__ weights, int topk, int E, int64_t N,
                                                          int64_t T, uint16_t* __restrict__ y) {
   tc::grid_dependency_wait();
@@ -1319,21 +1319,23 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict
   const int64_t per = N / kVec, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= T * per) return;
   const int64_t t = at / per, n = (at - t * per) * kVec;
+  const int32_t* id = ids + t * topk;
+  const float *wt = weights + t * topk, *first = yp + t * topk * N + n;
   float sum[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) sum[i] = 0.0f;
-  constexpr int kAhead = 8;  // pairs whose products are loaded before the first is added
+  constexpr int kAhead = 4;  // pairs whose products are loaded before the first is added (8: fewer warps fit, 3 % of a call)
   for (int j0 = 0; j0 < topk; j0 += kAhead) {
     float w[kAhead];
     bool use[kAhead];
     float4 v[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int e = j0 + j < topk ? __ldg(ids + t * topk + j0 + j) : -1;
+      const int e = j0 + j < topk ? __ldg(id + j0 + j) : -1;
       use[j] = e >= 0 && e < E;
-      w[j] = use[j] ? __ldg(weights + t * topk + j0 + j) : 0.0f;
+      w[j] = use[j] ? __ldg(wt + j0 + j) : 0.0f;
       if (!use[j]) continue;  // (not a product with zero: the place holds anything)
-      const float* src = yp + (t * topk + j0 + j) * N + n;
+      const float* src = first + (j0 + j) * N;
       if constexpr (kVec == 4)
         v[j] = *reinterpret_cast<const float4*>(src);
       else
